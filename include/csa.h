@@ -51,7 +51,7 @@ typedef enum {
   CSA_ERR_WORKSPACE = 3,     /* workspace missing or too small */
   CSA_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed */
   CSA_ERR_TIMEOUT = 5,       /* a bounded on-chip wait expired (device error word) */
-  CSA_ERR_DEVICE = 6         /* a kernel recorded a bad gather index */
+  CSA_ERR_DEVICE = 6         /* a kernel recorded a bad gather index or a missing page */
 } csa_status_t;
 
 typedef enum { CSA_F32 = 0, CSA_BF16 = 1, CSA_E4M3 = 2 } csa_dtype_t;
@@ -68,7 +68,8 @@ const char* csa_get_last_error_string(void);
 
 /* Synchronises `stream`, then reads and clears the device error words of the
  * current device.  Returns CSA_ERR_TIMEOUT or CSA_ERR_DEVICE if a kernel
- * recorded an expired wait or a bad gather index since the last check. */
+ * recorded an expired wait, a bad gather index or a missing page since the last
+ * check. */
 csa_status_t csa_check_device_error(cudaStream_t stream);
 
 /* Self-test of the failure path (no counterpart on the pages): launches one
@@ -388,6 +389,115 @@ csa_status_t csa_fused_attention_splitkv(const void* q, csa_dtype_t q_dtype, con
 csa_status_t csa_grouped_out_proj(const void* o, const void* w_grp, const void* w_out, int M, int H, int D,
                                   int G, int d_mid, int d_model, void* mid, void* out, csa_dtype_t out_dtype,
                                   cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged serving step.  The calls below take the new tokens of a ragged batch of
+ * decode steps and prompt chunks, and caches kept in pages.  The pages of the
+ * write-ups describe the layer, not its serving; the conventions here are this
+ * library's own.
+ *   Batch: cu_q [n_seq + 1] int32, ascending; sequence b has the batch rows
+ *     cu_q[b] .. cu_q[b+1] - 1 (none is allowed), at positions q_pos[b],
+ *     q_pos[b] + 1, ... (q_pos [n_seq] int64).  Both are DEVICE arrays.  Rows
+ *     behind cu_q[n_seq] (a padded batch) and rows at negative positions are
+ *     left as they were: their outputs are not written.
+ *   Pages: a cache is [n_pages, page_size, row] with page_size a power of two;
+ *     row p of sequence b is row p % page_size of page
+ *     block_table[b * max_pages + p / page_size] (int32, DEVICE).  Entries of
+ *     the table that no row needs may hold anything, -1 by custom.  A needed
+ *     entry outside [0, n_pages), or a row behind max_pages * page_size, is
+ *     recorded as CSA_ERR_DEVICE where a row is written; see the calls.  A dense
+ *     cache [n_seq, cap, D] with cap a multiple of page_size is one whose
+ *     table is b * cap / page_size + j.
+ *   Rotation: pair j < rope_dim / 2 turns by the angle p * inv_freq[j]
+ *     (inv_freq [rope_dim / 2] double, DEVICE; the angle is formed and reduced in
+ *     double) and is multiplied by mscale; (a, b) becomes
+ *     (a cos - b sin, a sin + b cos) * mscale.  Pairs of the rotated part
+ *     [rope_start, rope_start + rope_dim): interleaved 0: elements (j,
+ *     j + rope_dim / 2), 1: elements (2j, 2j + 1).  rope_dim is a multiple of 16
+ *     (0: no rotation), rope_start one of 8, D one of 16 in [16, 2048].
+ * Sums and rotations are in fp32; a result is rounded once, to its dtype.
+ * ------------------------------------------------------------------------- */
+
+/* csa_rope_freqs — frequencies of the rotation on the HOST, for
+ * cudaMemcpy to the device: w_j = base^(-2j / rope_dim), stretched for contexts
+ * `factor` (>= 1) times the trained one:
+ *   original_len = 0: every frequency divided by factor (linear), mscale 1;
+ *   original_len > 0: by parts (the published YaRN rule): with
+ *     turns = original_len * w_j / 2 pi and keep = (turns - beta_slow) /
+ *     (beta_fast - beta_slow) limited to [0, 1],
+ *     keep * w_j + (1 - keep) * w_j / factor; mscale = 0.1 ln(factor) + 1.
+ * inv_freq: rope_dim / 2 doubles.  No device call. */
+csa_status_t csa_rope_freqs(int rope_dim, double base, double factor, double original_len, double beta_fast,
+                            double beta_slow, double* inv_freq, float* mscale);
+
+/* csa_rope — rotates rows x [n_tok, H, D] (strides in elements, multiples of
+ * 16 bytes; innermost contiguous) into out (own strides); the other elements
+ * are copied.  out == x with the same dtype and strides rotates in place and
+ * touches the rotated part only; out may not overlap x otherwise.  inverse 1
+ * turns by the negative angle (the transpose of the rotation, which is also its
+ * gradient).  dtypes F32 or BF16. */
+csa_status_t csa_rope(const void* x, csa_dtype_t in_dtype, int64_t x_tok_stride, int64_t x_head_stride, int64_t n_tok,
+                      int H, int D, const int32_t* cu_q, const int64_t* q_pos, int n_seq, const double* inv_freq,
+                      int rope_dim, int rope_start, int interleaved, int inverse, float mscale, void* out,
+                      csa_dtype_t out_dtype, int64_t out_tok_stride, int64_t out_head_stride, cudaStream_t stream);
+
+/* csa_qk_norm_rope — RMSNorm over D (eps; gains fp32 [D] or NULL = 1) of the
+ * query rows q [n_tok, H, D] and the key rows k [n_tok, Hk, D], then their
+ * rotation, in one launch.  H or Hk may be 0 (its pointers are then ignored).
+ * Strides, dtypes and in-place outputs as csa_rope. */
+csa_status_t csa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t q_head_stride, int H, const void* k,
+                              int64_t k_tok_stride, int64_t k_head_stride, int Hk, csa_dtype_t in_dtype, int64_t n_tok,
+                              int D, const int32_t* cu_q, const int64_t* q_pos, int n_seq, const float* q_gain,
+                              const float* k_gain, float eps, const double* inv_freq, int rope_dim, int rope_start,
+                              int interleaved, float mscale, void* q_out, int64_t q_out_tok_stride,
+                              int64_t q_out_head_stride, void* k_out, int64_t k_out_tok_stride,
+                              int64_t k_out_head_stride, csa_dtype_t out_dtype, cudaStream_t stream);
+
+/* csa_paged_append — writes the batch's raw rows [n_tok, D] (row_stride in
+ * elements), normalised (norm 1, gain fp32 [D] or NULL) and rotated (last
+ * rope_dim dims), into their rows of a paged cache.  page_dtype
+ *   BF16, F32: pages [n_pages, page_size, D];
+ *   E4M3: pages u8 [.., D - 64] codes of x / s with s = max|x[:D - 64]| / 448
+ *         (1 for zeros), pages_rope bf16 [.., 64], pages_scale fp32
+ *         [n_pages, page_size] = s (needs rope_dim 64): the row format of
+ *         csa_compress_append.
+ * A row without a page is not written and recorded as CSA_ERR_DEVICE.  A page
+ * that is written belongs to one sequence. */
+csa_status_t csa_paged_append(const void* rows, csa_dtype_t in_dtype, int64_t row_stride, int64_t n_tok, int D,
+                              const int32_t* cu_q, const int64_t* q_pos, int n_seq, const int32_t* block_table,
+                              int max_pages, int page_size, int64_t n_pages, int norm, const float* gain, float eps,
+                              const double* inv_freq, int rope_dim, int interleaved, float mscale, void* pages,
+                              csa_dtype_t page_dtype, void* pages_rope, float* pages_scale, cudaStream_t stream);
+
+/* csa_paged_attention — attention of the batch's new tokens over their
+ * sequences' paged caches: shared K = V rows, one softmax over
+ *   the entries i of the entry pages with (i + 1) * m - 1 <= p (as
+ *     hca_dense_attn; m = 1: every row up to p), kv_pages NULL: none;
+ *   the raw rows max(0, p - W + 1) .. p of the token pages (W = 0: 0 .. p),
+ *     tok_pages NULL: none;
+ *   and the sink of the head (fp32 [H] or NULL).
+ * The token's own raw row must be in its page before the call
+ * (csa_paged_append).  A token that sees no row yields 0.
+ *   q [n_tok, H, D] BF16, normalised and rotated; H in [1, 64]; D 128 or 512.
+ *   tok_pages [n_tok_pages, tok_page_size, D] BF16.
+ *   kv_pages [n_kv_pages, kv_page_size, D] BF16, or E4M3 with kv_rope and
+ *     kv_scale (the row format of csa_paged_append).
+ *   out [n_tok, H, D] F32 or BF16: bf16 tensor-core products (probabilities
+ *     rounded to bf16), fp32 accumulation and softmax statistics.
+ * Rows that a token does not see never reach its output, whatever they hold.
+ * A visible row without a page is recorded as CSA_ERR_DEVICE and read as zeros;
+ * rows behind max_pages * page_size are not visible.
+ * workspace: csa_paged_attention_workspace(n_tok, n_seq, H, D) bytes (0 from
+ * about 75 tokens on), 16-byte aligned; calls sharing one must be ordered on
+ * one stream, and a captured graph keeps its own. */
+size_t csa_paged_attention_workspace(int64_t n_tok, int n_seq, int H, int D);
+csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H, int D, const int32_t* cu_q, const int64_t* q_pos,
+                                 int n_seq, const void* tok_pages, const int32_t* tok_table, int tok_max_pages,
+                                 int64_t n_tok_pages, int tok_page_size, int W, const void* kv_pages,
+                                 csa_dtype_t kv_dtype, const void* kv_rope, const float* kv_scale,
+                                 const int32_t* kv_table, int kv_max_pages, int64_t n_kv_pages, int kv_page_size, int m,
+                                 const float* sink, float scale, void* workspace, size_t ws_bytes, void* out,
+                                 csa_dtype_t out_dtype, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -10,8 +10,11 @@ Entry points (same names as the C ABI):
   csa_sparse_mqa, hca_dense_attn, swa_sink_combine, csa_fused_attention,
   csa_fused_attention_splitkv (n_split > 1), csa_index_topk_fp4, csa_cache_append,
   csa_grouped_out_proj
+and, for ragged batches over paged caches,
+  csa_rope_freqs, csa_rope, csa_qk_norm_rope, csa_paged_append, csa_paged_attention
 and compositions of them: csa_layer_prefill, hca_layer_prefill,
-swa_layer_prefill, csa_layer_decode, hca_layer_decode, swa_layer_decode.
+swa_layer_prefill, csa_layer_decode, hca_layer_decode, swa_layer_decode,
+paged_layer_step.
 """
 from __future__ import annotations
 
@@ -43,6 +46,7 @@ def lib():
         raise CsaError(f"{LIB_PATH} is not built; run `python -m long_context_compressed_02_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
     P, I, I64, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    DB = ctypes.c_double
     sig = {
         "csa_abi_version": ([], I),
         "csa_status_string": ([I], ctypes.c_char_p),
@@ -68,6 +72,14 @@ def lib():
         "csa_selftest_wait_timeout": ([ctypes.c_uint64, P], I),
         "csa_cache_append": ([P, P, I, P, I, I, I, I, P, P, P, P, P, P, I64, I, F, F, P, P, P, I, P, P, P, P, P], I),
         "csa_index_topk_fp4_workspace": ([I, I, I, I64, I], SZ),
+        "csa_rope_freqs": ([I, DB, DB, DB, DB, DB, P, P], I),
+        "csa_rope": ([P, I, I64, I64, I64, I, I, P, P, I, P, I, I, I, I, F, P, I, I64, I64, P], I),
+        "csa_qk_norm_rope": ([P, I64, I64, I, P, I64, I64, I, I, I64, I, P, P, I, P, P, F, P, I, I, I, F, P, I64, I64,
+                              P, I64, I64, I, P], I),
+        "csa_paged_append": ([P, I, I64, I64, I, P, P, I, P, I, I, I64, I, P, F, P, I, I, F, P, I, P, P, P], I),
+        "csa_paged_attention_workspace": ([I64, I, I, I], SZ),
+        "csa_paged_attention": ([P, I64, I, I, P, P, I, P, P, I, I64, I, I, P, I, P, P, P, I, I64, I, I, P, F, P, SZ, P,
+                                 I, P], I),
         "csa_index_topk_fp4": ([P, P, P, P, P, P, I, I, I, I64, I, I, P, P, SZ, P], I),
     }
     for name, (args, res) in sig.items():
@@ -376,6 +388,296 @@ def csa_grouped_out_proj(o, w_grp, w_out, *, mid=None, out=None, out_dtype=torch
     return (out, mid) if return_mid else out
 
 
+# ---------------------------------------------------------------- paged serving step
+
+def _batch_args(what, dev, cu_q, q_pos, **tensors):
+    """Checks what the paged calls share: every tensor on device `dev`, cu_q
+    [n_seq + 1] int32 and q_pos [n_seq] int64.  Returns n_seq."""
+    for n, t in dict(cu_q=cu_q, q_pos=q_pos, **tensors).items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise CsaError(f"{what}: {n} must be a CUDA tensor")
+        if t.device != dev:
+            raise CsaError(f"{what}: {n} is on {t.device}, not {dev}")
+    if cu_q.dtype != torch.int32 or q_pos.dtype != torch.int64 or q_pos.dim() != 1 or \
+            tuple(cu_q.shape) != (q_pos.shape[0] + 1,) or not (cu_q.is_contiguous() and q_pos.is_contiguous()):
+        raise CsaError(f"{what}: cu_q [n_seq + 1] int32 and q_pos [n_seq] int64, contiguous, expected")
+    return q_pos.shape[0]
+
+
+class _on:
+    """Makes a tensor's device current, and on it the given stream (else that
+    device's current one), so that what a call allocates belongs to the stream
+    that it launches on.  Yields the stream handle."""
+
+    def __init__(self, dev, stream):
+        self.dev = torch.cuda.device(dev)
+        self.stream = stream
+
+    def __enter__(self):
+        self.dev.__enter__()
+        if self.stream is None:
+            self.ctx = None
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        self.ctx = torch.cuda.stream(self.stream)
+        self.ctx.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        self.dev.__exit__(*exc)
+
+
+def _float_dtype(what, name, t):
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise CsaError(f"{what}: {name} must be float32 or bfloat16")
+
+
+def _heads(what, name, t, out=False):
+    """(t as [n, H, D], token stride, head stride) of rows [n, H, D] or [n, D]."""
+    if t.dim() == 2:
+        t = t.unsqueeze(1)
+    if t.dim() != 3:
+        raise CsaError(f"{what}: {name} must be [n_tok, H, D] or [n_tok, D]")
+    _float_dtype(what, name, t)
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise CsaError(f"{what}: the last dimension of {name} must be contiguous")
+    ts = t.stride(0) if t.shape[0] > 1 else 0
+    hs = t.stride(1) if t.shape[1] > 1 else 0
+    if out and t.numel():
+        D = t.shape[2]
+        used = sorted((s, n) for s, n in ((ts, t.shape[0]), (hs, t.shape[1])) if n > 1)
+        if used and (used[0][0] < D or (len(used) == 2 and used[1][0] < used[0][0] * (used[0][1] - 1) + D)):
+            raise CsaError(f"{what}: the rows of {name} overlap")
+    return t, ts, hs
+
+
+def _freqs(what, inv_freq):
+    if inv_freq is None:
+        return 0
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise CsaError(f"{what}: inv_freq must be a contiguous float64 [rope_dim / 2]")
+    return 2 * inv_freq.shape[0]
+
+
+def _gain(what, name, g, D):
+    if g is not None and (g.dtype != torch.float32 or tuple(g.shape) != (D,) or not g.is_contiguous()):
+        raise CsaError(f"{what}: {name} must be a contiguous float32 [{D}]")
+
+
+def _shares(a, b):
+    """Whether two tensors may share memory without being the same view.  Views
+    of one buffer that take other parts of each of its rows do not."""
+    if a.untyped_storage().data_ptr() != b.untyped_storage().data_ptr() or not (a.numel() and b.numel()):
+        return False
+    if a.data_ptr() == b.data_ptr() and a.dtype == b.dtype and a.shape == b.shape and \
+            all(s == u or n == 1 for n, s, u in zip(a.shape, a.stride(), b.stride())):
+        return False
+
+    def extent(t, dims):
+        return (sum((n - 1) * s for n, s in zip(t.shape[dims:], t.stride()[dims:])) + 1) * t.element_size()
+    lo = b.data_ptr() - a.data_ptr()
+    if lo >= extent(a, 0) or -lo >= extent(b, 0):
+        return False
+    row = a.stride(0) * a.element_size()
+    if a.dim() > 1 and b.dim() > 1 and row > 0 and row == b.stride(0) * b.element_size():
+        at = lo % row
+        return not (at >= extent(a, 1) and at + extent(b, 1) <= row)
+    return True
+
+
+def csa_rope_freqs(rope_dim, *, base=10000.0, factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0,
+                   device="cuda"):
+    """Frequencies of the rotation, (inv_freq [rope_dim / 2] float64 on `device`,
+    mscale): base^(-2j / rope_dim), stretched for a context `factor` times the
+    trained one: linearly (original_len 0), or by parts from the trained length."""
+    w = (ctypes.c_double * max(1, int(rope_dim) // 2))()
+    ms = ctypes.c_float()
+    _check(lib().csa_rope_freqs(int(rope_dim), base, factor, float(original_len), beta_fast, beta_slow,
+                                ctypes.cast(w, ctypes.c_void_p), ctypes.cast(ctypes.pointer(ms), ctypes.c_void_p)),
+           "csa_rope_freqs")
+    return torch.tensor(list(w), dtype=torch.float64, device=device), ms.value
+
+
+def csa_rope(x, cu_q, q_pos, inv_freq, *, rope_start=None, interleaved=False, inverse=False, mscale=1.0,
+             out_dtype=None, out=None, stream=None):
+    """Rotary positions of the rows x [n_tok, H, D] (or [n_tok, D], any strides
+    of 16 bytes) of a ragged batch: the pairs of the part that starts at
+    rope_start (default: the last rope_dim elements) turn by position *
+    inv_freq and scale by mscale.  out=x rotates in place."""
+    what = "csa_rope"
+    n_seq = _batch_args(what, x.device, cu_q, q_pos, x=x, inv_freq=inv_freq, out=out)
+    x3, xt, xh = _heads(what, "x", x)
+    r = _freqs(what, inv_freq)
+    n, H, D = x3.shape
+    with _on(x.device, stream) as st:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise CsaError(f"{what}: out must have x's shape and out_dtype")
+        o3, ot, oh = _heads(what, "out", out, out=True)
+        if _shares(x, out):
+            raise CsaError(f"{what}: out must be x itself or not overlap it")
+        _check(lib().csa_rope(_ptr(x), _DT[x.dtype], xt, xh, n, H, D, _ptr(cu_q), _ptr(q_pos), n_seq, _ptr(inv_freq), r,
+                              D - r if rope_start is None else rope_start, int(interleaved), int(inverse), mscale,
+                              _ptr(out), _DT[out.dtype], ot, oh, st), what)
+    return out
+
+
+def csa_qk_norm_rope(q, k, cu_q, q_pos, inv_freq, *, q_gain=None, k_gain=None, rope_start=None, interleaved=False,
+                     mscale=1.0, eps=1e-6, out_dtype=None, q_out=None, k_out=None, stream=None):
+    """RMSNorm of the query rows q [n_tok, H, D] and the key rows k [n_tok, Hk, D]
+    (or [n_tok, D], or None) with gains [D] float32, and their rotation, in one
+    launch; views of one projection's output are read in place.  Returns
+    (q_out, k_out)."""
+    what = "csa_qk_norm_rope"
+    n_seq = _batch_args(what, q.device, cu_q, q_pos, q=q, k=k, inv_freq=inv_freq, q_gain=q_gain, k_gain=k_gain,
+                        q_out=q_out, k_out=k_out)
+    r = _freqs(what, inv_freq)
+    q3, qt, qh = _heads(what, "q", q)
+    n, H, D = q3.shape
+    _gain(what, "q_gain", q_gain, D)
+    _gain(what, "k_gain", k_gain, D)
+    with _on(q.device, stream) as st:
+        outs = []
+        for name, x, o in (("q", q, q_out), ("k", k, k_out)):
+            if x is None:
+                if o is not None:
+                    raise CsaError(f"{what}: {name}_out without {name}")
+                outs.append((None, 0, 0, None, 0, 0, 0))
+                continue
+            x3, xt, xh = _heads(what, name, x)
+            if x3.shape[0] != n or x3.shape[2] != D or x.dtype != q.dtype:
+                raise CsaError(f"{what}: q [n_tok, H, D] and k [n_tok, Hk, D] of one dtype expected")
+            if o is None:
+                o = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+            elif o.shape != x.shape or (out_dtype is not None and o.dtype != out_dtype):
+                raise CsaError(f"{what}: {name}_out must have the shape of {name} and out_dtype")
+            _, ot, oh = _heads(what, name + "_out", o, out=True)
+            outs.append((x, xt, xh, o, ot, oh, x3.shape[1]))
+        (_, qt, qh, qo, qot, qoh, H), (_, kt, kh, ko, kot, koh, Hk) = outs
+        if ko is not None and ko.dtype != qo.dtype:
+            raise CsaError(f"{what}: the outputs must have one dtype")
+        for o in (qo, ko):
+            for x in (q, k):
+                if o is not None and x is not None and _shares(x, o):
+                    raise CsaError(f"{what}: an output must be its input itself or overlap neither input")
+        if ko is not None and (_shares(qo, ko) or (qo.data_ptr() == ko.data_ptr() and qo.numel() > 0)):
+            raise CsaError(f"{what}: the outputs overlap")
+        _check(lib().csa_qk_norm_rope(_ptr(q), qt, qh, H, _ptr(k), kt, kh, Hk, _DT[q.dtype], n, D, _ptr(cu_q),
+                                      _ptr(q_pos), n_seq, _ptr(q_gain), _ptr(k_gain), eps, _ptr(inv_freq), r,
+                                      D - r if rope_start is None else rope_start, int(interleaved), mscale, _ptr(qo),
+                                      qot, qoh, _ptr(ko), kot, koh, _DT[qo.dtype], st), what)
+    return qo, ko
+
+
+def _table(what, name, table, n_seq):
+    if table is None or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_seq or \
+            not table.is_contiguous():
+        raise CsaError(f"{what}: {name} must be a contiguous int32 [n_seq, max_pages]")
+
+
+def _e4m3_pages(what, pages, rope, scale, D):
+    if rope is None or scale is None or rope.dtype != torch.bfloat16 or scale.dtype != torch.float32 or \
+            pages.shape[2] + 64 != D or tuple(rope.shape) != (*pages.shape[:2], 64) or \
+            tuple(scale.shape) != tuple(pages.shape[:2]) or not (rope.is_contiguous() and scale.is_contiguous()):
+        raise CsaError(f"{what}: e4m3 pages are [n_pages, page_size, D - 64] uint8 with [.., 64] bfloat16 and "
+                       "[n_pages, page_size] float32")
+
+
+def csa_paged_append(rows, cu_q, q_pos, block_table, pages, inv_freq, *, pages_rope=None, pages_scale=None, norm=True,
+                     gain=None, interleaved=False, mscale=1.0, eps=1e-6, stream=None):
+    """Appends the raw rows [n_tok, D] of a ragged batch, normalised and rotated
+    (inv_freq None: not rotated), to a paged cache: pages [n_pages, page_size, D]
+    bfloat16 or float32, or uint8 e4m3 codes [n_pages, page_size, D - 64] with
+    pages_rope [.., 64] bfloat16 and pages_scale [n_pages, page_size] float32."""
+    what = "csa_paged_append"
+    n_seq = _batch_args(what, rows.device, cu_q, q_pos, rows=rows, block_table=block_table, pages=pages,
+                        inv_freq=inv_freq, pages_rope=pages_rope, pages_scale=pages_scale, gain=gain)
+    if rows.dim() != 2:
+        raise CsaError(f"{what}: rows must be [n_tok, D]")
+    _, rt, _ = _heads(what, "rows", rows)
+    n, D = rows.shape
+    r = _freqs(what, inv_freq)
+    _gain(what, "gain", gain, D)
+    _table(what, "block_table", block_table, n_seq)
+    if pages.dim() != 3 or pages.dtype not in _DT or not pages.is_contiguous():
+        raise CsaError(f"{what}: pages must be contiguous [n_pages, page_size, D] bfloat16 or float32, or uint8 codes")
+    if pages.dtype == torch.uint8:
+        _e4m3_pages(what, pages, pages_rope, pages_scale, D)
+    elif pages.shape[2] != D or pages_rope is not None or pages_scale is not None:
+        raise CsaError(f"{what}: pages [n_pages, page_size, {D}] without rope and scale pages expected")
+    for p in (pages, pages_rope, pages_scale):
+        if p is not None and (_shares(rows, p) or (p.numel() and p.data_ptr() == rows.data_ptr())):
+            raise CsaError(f"{what}: rows and pages overlap")
+    with _on(rows.device, stream) as st:
+        _check(lib().csa_paged_append(_ptr(rows), _DT[rows.dtype], rt, n, D, _ptr(cu_q), _ptr(q_pos), n_seq,
+                                      _ptr(block_table), block_table.shape[1], pages.shape[1], pages.shape[0],
+                                      int(norm), _ptr(gain), eps, _ptr(inv_freq), r, int(interleaved), mscale,
+                                      _ptr(pages), _DT[pages.dtype], _ptr(pages_rope), _ptr(pages_scale), st), what)
+
+
+def csa_paged_attention_workspace(n_tok, n_seq, H, D):
+    return int(lib().csa_paged_attention_workspace(n_tok, n_seq, H, D))
+
+
+def csa_paged_attention(q, cu_q, q_pos, *, tok_pages=None, tok_table=None, W=128, kv_pages=None, kv_rope=None,
+                        kv_scale=None, kv_table=None, m=128, sink=None, scale=None, out_dtype=None, out=None,
+                        workspace=None, stream=None):
+    """Attention of the new tokens q [n_tok, H, D] bfloat16 of a ragged batch over
+    paged shared K = V rows: the complete entries (ratio m) of kv_pages (bfloat16
+    [n_pages, page_size, D], or e4m3 with kv_rope and kv_scale) and the last W raw
+    rows (0: all) of tok_pages, with the sink [H] in one softmax.  Either cache
+    may be absent.  The tokens' own raw rows are in their pages already."""
+    what = "csa_paged_attention"
+    n_seq = _batch_args(what, q.device, cu_q, q_pos, q=q, tok_pages=tok_pages, tok_table=tok_table, kv_pages=kv_pages,
+                        kv_rope=kv_rope, kv_scale=kv_scale, kv_table=kv_table, sink=sink, out=out, workspace=workspace)
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise CsaError(f"{what}: q must be a contiguous bfloat16 [n_tok, H, D]")
+    n, H, D = q.shape
+    if tok_pages is not None:
+        _table(what, "tok_table", tok_table, n_seq)
+        if tok_pages.dim() != 3 or tok_pages.dtype != torch.bfloat16 or tok_pages.shape[2] != D or \
+                not tok_pages.is_contiguous():
+            raise CsaError(f"{what}: tok_pages must be a contiguous bfloat16 [n_pages, page_size, {D}]")
+    if kv_pages is not None:
+        _table(what, "kv_table", kv_table, n_seq)
+        if kv_pages.dim() != 3 or not kv_pages.is_contiguous() or kv_pages.dtype not in (torch.bfloat16, torch.uint8):
+            raise CsaError(f"{what}: kv_pages must be contiguous [n_pages, page_size, D] bfloat16 or uint8 codes")
+        if kv_pages.dtype == torch.uint8:
+            _e4m3_pages(what, kv_pages, kv_rope, kv_scale, D)
+        elif kv_pages.shape[2] != D or kv_rope is not None or kv_scale is not None:
+            raise CsaError(f"{what}: kv_pages [n_pages, page_size, {D}] without rope and scale pages expected")
+    if sink is not None and (sink.dtype != torch.float32 or tuple(sink.shape) != (H,) or not sink.is_contiguous()):
+        raise CsaError(f"{what}: sink must be a contiguous float32 [{H}]")
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    with _on(q.device, stream) as st:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+        if out.shape != q.shape or out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or \
+                (out_dtype is not None and out.dtype != out_dtype):
+            raise CsaError(f"{what}: out must be contiguous, of q's shape, float32 or bfloat16")
+        if any(t is not None and n and (_shares(t, out) or t.data_ptr() == out.data_ptr())
+               for t in (q, tok_pages, kv_pages, kv_rope)):
+            raise CsaError(f"{what}: out overlaps an input")
+        if workspace is None:
+            need = csa_paged_attention_workspace(n, n_seq, H, D)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        elif not workspace.is_contiguous():
+            raise CsaError(f"{what}: workspace must be contiguous")
+        tp, tn, ts = (tok_table.shape[1], tok_pages.shape[0], tok_pages.shape[1]) if tok_pages is not None else (0, 0, 0)
+        kp, kn, ks = (kv_table.shape[1], kv_pages.shape[0], kv_pages.shape[1]) if kv_pages is not None else (0, 0, 0)
+        _check(lib().csa_paged_attention(
+            _ptr(q), n, H, D, _ptr(cu_q), _ptr(q_pos), n_seq, _ptr(tok_pages), _ptr(tok_table), tp, tn, ts, W,
+            _ptr(kv_pages), BF16 if kv_pages is None else _DT[kv_pages.dtype], _ptr(kv_rope), _ptr(kv_scale),
+            _ptr(kv_table), kp, kn, ks, m, _ptr(sink), scale, _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(out), _DT[out.dtype], st),
+            what)
+    return out
+
+
 # ---------------------------------------------------------------- layers
 
 def csa_layer_prefill(q, C, Z, B, qI, w, kI, sink, *, k, m=4, W=128, norm_rope=False, inv_rope=False,
@@ -478,3 +780,25 @@ def hca_layer_decode(lay, q_pos, *, m=128, W=128, n_split=1, out=None, attn_work
                                kv_rope=lay["kv_rope"], kv_scale=lay["kv_scale"], window_mode=1, inv_rope=True,
                                rope_dim=lay["kv_rope"].shape[-1], out=out, n_split=n_split,
                                workspace=attn_workspace, stream=stream)
+
+
+def paged_layer_step(q, rows, cu_q, q_pos, inv_freq, tok_pages, tok_table, *, W=128, sink=None, q_gain=None, gain=None,
+                     kv_pages=None, kv_rope=None, kv_scale=None, kv_table=None, m=128, interleaved=False, mscale=1.0,
+                     inv_rope=True, eps=1e-6, workspace=None, stream=None):
+    """One layer, one serving step of a ragged batch (decode tokens and prompt
+    chunks together) over paged caches: the queries q [n_tok, H, D] are
+    normalised and rotated, the raw rows [n_tok, D] appended to their token
+    pages, the new tokens attend the window (W, 0: all raw rows) and, if
+    kv_pages is given, the complete entries (a heavily compressed layer), and the
+    rotated part of the output is turned back (inv_rope)."""
+    qn, _ = csa_qk_norm_rope(q, None, cu_q, q_pos, inv_freq, q_gain=q_gain, interleaved=interleaved, mscale=mscale,
+                             eps=eps, out_dtype=torch.bfloat16, stream=stream)
+    csa_paged_append(rows, cu_q, q_pos, tok_table, tok_pages, inv_freq, gain=gain, interleaved=interleaved,
+                     mscale=mscale, eps=eps, stream=stream)
+    out = csa_paged_attention(qn, cu_q, q_pos, tok_pages=tok_pages, tok_table=tok_table, W=W, kv_pages=kv_pages,
+                              kv_rope=kv_rope, kv_scale=kv_scale, kv_table=kv_table, m=m, sink=sink,
+                              workspace=workspace, stream=stream)
+    if inv_rope:
+        csa_rope(out, cu_q, q_pos, inv_freq, interleaved=interleaved, inverse=True, mscale=1.0 / mscale, out=out,
+                 stream=stream)
+    return out

@@ -44,12 +44,14 @@
 // SMs, claimed from a counter so that ranges of unequal length balance.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math_constants.h>
 #include "common.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
+#include "batch.cuh"
 
 namespace csa {
 
@@ -111,6 +113,12 @@ struct AttnParams {
   int per_item;                 // > 0: half chunks per range, the same for every token (ranges past a
                                 // token's rows are empty); 0: each token's rows cut into n_split ranges
   uint32_t* item_counter;       // non-null: items are claimed dynamically from this zeroed counter
+  // paged form: a ragged batch over paged caches (cap, cap2: rows that the block tables can name)
+  const int32_t* cu_q;          // [n_seq + 1]
+  int64_t n_tok;
+  PageTable pt1, pt2;
+  int max_items;                // > 0: the rows are cut into at most this many ranges (see SplitPlan)
+  int32_t* plan;                // [n_seq + 1] first range of each sequence, for the merge
 };
 
 // Rows are consumed in half chunks of 64 (one ring slot each).  The window
@@ -143,18 +151,21 @@ __device__ __forceinline__ int count_valid_warp(const int32_t* row, int k, int l
   return s1;
 }
 
-// Whole-warp call: every lane gets the same row set.
-__device__ __forceinline__ RowSet row_set_warp(const AttnParams& p, int b, int t, int sp, int lane) {
+// Whole-warp call: every lane gets the same row set.  `per_plan`: half chunks
+// per range of a paged call (0: the whole row set is one range).
+template <bool PAGED = false>
+__device__ __forceinline__ RowSet row_set_warp(const AttnParams& p, int b, int t, int sp, int lane, int per_plan = 0) {
   RowSet r{0, 0, 0, 0, 0, 0, 0, 0, nullptr};
   const int64_t pos = (p.q_pos ? p.q_pos[b] : 0) + t;
   if (p.src1 == SRC1_GATHER) {
     r.idx = p.idx + ((int64_t)b * p.T + t) * p.k;
     r.n1 = count_valid_warp(r.idx, p.k, lane);
   } else if (p.src1 == SRC1_DENSE) {
-    r.n1 = (int)min(p.cap, (pos + 1) / p.m);
+    r.n1 = PAGED ? (int)max((int64_t)0, min(p.cap, (pos + 1) / p.m)) : (int)min(p.cap, (pos + 1) / p.m);
   }
   if (p.src2 == SRC2_WINDOW) {
-    const int64_t lo = max((int64_t)0, pos - p.W + 1), hi = min(p.cap2, pos + 1);
+    // W = 0 (paged calls only): every row up to the position
+    const int64_t lo = (PAGED && p.W == 0) ? 0 : max((int64_t)0, pos - p.W + 1), hi = min(p.cap2, pos + 1);
     r.lo2 = lo;
     r.n2 = (int)max((int64_t)0, hi - lo);
   } else if (p.src2 == SRC2_CACHE) {
@@ -164,10 +175,106 @@ __device__ __forceinline__ RowSet row_set_warp(const AttnParams& p, int b, int t
   r.n = r.n1 + r.n2;
   r.nh2 = (r.n2 + kRows - 1) / kRows;
   r.nh = r.nh2 + (r.n1 + kRows - 1) / kRows;
-  const int per = p.per_item > 0 ? p.per_item : (r.nh + p.n_split - 1) / p.n_split;
+  const int per = PAGED ? (per_plan > 0 ? per_plan : r.nh)
+                        : (p.per_item > 0 ? p.per_item : (r.nh + p.n_split - 1) / p.n_split);
   r.c0 = min(r.nh, sp * per);
   r.c1 = min(r.nh, r.c0 + per);
   return r;
+}
+
+// Half chunks of the row set of a paged call's query at position pos.
+__device__ __forceinline__ int paged_half_chunks(const AttnParams& p, int64_t pos) {
+  int64_t n1 = 0, n2 = 0;
+  if (p.src1 == SRC1_DENSE) n1 = max((int64_t)0, min(p.cap, (pos + 1) / p.m));
+  if (p.src2 == SRC2_WINDOW)
+    n2 = max((int64_t)0, min(p.cap2, pos + 1) - (p.W == 0 ? 0 : max((int64_t)0, pos - p.W + 1)));
+  return (int)((n1 + kRows - 1) / kRows + (n2 + kRows - 1) / kRows);
+}
+
+// Work items of a paged call with few query tokens.  Every row set is cut into
+// ranges of `per` half chunks; sequence b's tokens take ranges first[b] ..
+// first[b + 1] - 1, the same number each (that of its last token).  `per` is
+// the smallest step of the search below that leaves at most max_items ranges,
+// one for each SM, so that the call is one wave whatever the lengths are: they
+// are known on the device only.  Without empty ranges to step over, an item
+// costs a CTA nothing but its rows.  Whole-CTA call.
+constexpr int kPlanSeqs = 1024;    // sequences that the shared-memory plan holds
+struct SplitPlan {
+  int32_t first[kPlanSeqs + 1];
+  int32_t nh[kPlanSeqs];           // half chunks of the sequence's last token
+  int per;
+};
+__device__ __forceinline__ void make_plan(const AttnParams& p, SplitPlan& s, int tid, int nthreads) {
+  for (int b = tid; b < p.n_seq; b += nthreads) {
+    const int len = p.cu_q[b + 1] - p.cu_q[b];
+    // a token without rows still has one (empty) range, which tells the merge so
+    s.nh[b] = len > 0 ? max(1, paged_half_chunks(p, p.q_pos[b] + len - 1)) : 0;
+    s.first[b] = max(0, len);      // the lengths, until the prefix sums replace them
+  }
+  __syncthreads();
+  if (tid < 32) {
+    auto sum = [&](int per) {      // per = 0: all half chunks; else the ranges
+      int64_t n = 0;
+      for (int b = tid; b < p.n_seq; b += 32)
+        n += (int64_t)s.first[b] * (per ? (s.nh[b] + per - 1) / per : s.nh[b]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      return n;
+    };
+    const int64_t all = sum(0);
+    int64_t per = max((int64_t)1, (all + p.max_items - 1) / p.max_items);
+    // ends: from per = all on there is one range for each token, at most max_items
+    while (per < all && sum((int)per) > p.max_items) per += max((int64_t)1, per >> 4);
+    per = min(per, max((int64_t)1, all));
+    int at = 0;                    // exclusive prefix sums, 32 sequences a step
+    for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+      const int b = b0 + tid;
+      const int n = b < p.n_seq ? s.first[b] * (int)((s.nh[b] + per - 1) / per) : 0;
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (tid >= o) inc += v;
+      }
+      if (b < p.n_seq) s.first[b] = at + inc - n;
+      at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (tid == 0) { s.first[p.n_seq] = at; s.per = (int)per; }
+  }
+  __syncthreads();
+}
+
+// Item -> sequence, token of the sequence, range, row of the batch.  A paged
+// call's item may be a padding row, which belongs to no sequence (false).
+struct Item { int b, t, sp; int64_t bt; int per; };
+template <bool PAGED>
+__device__ __forceinline__ bool locate_warp(const AttnParams& p, const SplitPlan* plan, int64_t item, int lane, Item& it) {
+  if constexpr (PAGED) {
+    it.sp = 0;
+    it.per = 0;
+    if (plan) {
+      it.b = find_seq_warp(plan->first, p.n_seq, item, lane);
+      if (it.b < 0) return false;
+      const int c0 = p.cu_q[it.b], len = p.cu_q[it.b + 1] - c0;
+      const int f0 = plan->first[it.b], ns = (plan->first[it.b + 1] - f0) / len;
+      it.t = (int)(item - f0) / ns;
+      it.sp = (int)(item - f0) % ns;
+      it.bt = c0 + it.t;
+      it.per = plan->per;
+      return it.bt >= 0 && it.bt < p.n_tok;
+    }
+    it.bt = item;
+    it.b = find_seq_warp(p.cu_q, p.n_seq, item, lane);
+    if (it.b < 0) return false;
+    it.t = (int)(item - p.cu_q[it.b]);
+  } else {
+    it.bt = item / p.n_split;
+    it.sp = (int)(item % p.n_split);
+    it.b = (int)(it.bt / p.T);
+    it.t = (int)(it.bt % p.T);
+    it.per = 0;
+  }
+  return true;
 }
 
 // mbarrier.try_wait suspends the thread in hardware until the phase completes
@@ -273,7 +380,7 @@ __device__ __forceinline__ float2 col_reduce16(float (&v)[16], int lane) {
   return make_float2(v[0], v[1]);
 }
 
-template <int D, int KV, int EPI>
+template <int D, int KV, int EPI, bool PAGED = false>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_q,
             const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_tok) {
@@ -337,7 +444,16 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   volatile int* abort_flag = s_abort;
-  const int64_t n_items = (int64_t)p.n_seq * p.T * p.n_split;
+  // a paged call with few tokens: its plan behind the other shared memory
+  SplitPlan* plan = nullptr;
+  if (PAGED && p.max_items > 0) {
+    plan = reinterpret_cast<SplitPlan*>(s_abort + 1);
+    make_plan(p, *plan, tid, kThreads);
+    if (blockIdx.x == 0)
+      for (int b = tid; b <= p.n_seq; b += kThreads) p.plan[b] = plan->first[b];
+  }
+  const int64_t n_items = !PAGED ? (int64_t)p.n_seq * p.T * p.n_split
+                                 : plan ? min(plan->first[p.n_seq], p.max_items) : p.n_tok;
   // Item sequence k = 0, 1, ... of this CTA: grid-stride, or (with a counter)
   // claimed by one loader thread with an atomic and handed to every role warp
   // through a 4-slot ring, so CTAs that drew short items take more of them.
@@ -367,10 +483,11 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     for (uint32_t kk = 0; ok; ++kk) {
       const int64_t item = get_item(kk, lt == 0);
       if (item >= n_items) break;
-      const int64_t bt = item / p.n_split;
-      const int sp = (int)(item % p.n_split);
-      const int b = (int)(bt / p.T), t = (int)(bt % p.T);
-      const RowSet rs = row_set_warp(p, b, t, sp, lane);
+      Item it;
+      if (!locate_warp<PAGED>(p, plan, item, lane, it)) continue;
+      const int b = it.b, t = it.t;
+      const int64_t bt = it.bt;
+      const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per);
       if (rs.c1 <= rs.c0) continue;
       // ---- Q tile: 64 rows x NS slabs of 128 B
       if (!wait_bar(q_free, (qcount & 1) ^ 1, abort_flag)) { ok = false; break; }
@@ -382,7 +499,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           mbar_expect_tx(q_full, kNQ * D * 2);
 #pragma unroll 1
           for (int s = 0; s < NS; ++s)
-            tma_load_2d(sQ + s * kQSlab, &map_q, 64 * s, (int32_t)(((int64_t)b * p.T + t) * p.H), q_full);
+            tma_load_2d(sQ + s * kQSlab, &map_q, 64 * s, (int32_t)(bt * p.H), q_full);
         } else {
           mbar_arrive(q_full);
         }
@@ -391,7 +508,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           for (int u = lt; u < kNQ * NS; u += 128) {
             const int r = u % kNQ, s = u / kNQ;
             const bool v = r < p.H;
-            const int64_t qrow = ((int64_t)b * p.T + t) * p.H + (v ? r : 0);
+            const int64_t qrow = bt * p.H + (v ? r : 0);
             const float* src = reinterpret_cast<const float*>(p.q) + qrow * D + 64 * s;
             float x[64];
 #pragma unroll
@@ -404,7 +521,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         } else {
           // consecutive lanes take consecutive 16-byte pieces of one query row
           constexpr int kPieces = D / 8;                       // 16-byte pieces per row
-          const uint8_t* qb = reinterpret_cast<const uint8_t*>(p.q) + ((int64_t)b * p.T + t) * p.H * D * 2;
+          const uint8_t* qb = reinterpret_cast<const uint8_t*>(p.q) + bt * p.H * D * 2;
           for (int u = lt; u < kNQ * kPieces; u += 128) {
             const int r = u / kPieces, c = u % kPieces;
             const bool v = r < p.H;
@@ -418,7 +535,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       }
       // ---- KV half chunks into the two-slot ring
       int pre_c = -1;                    // half chunk whose gathered row index pre_row holds
-      int32_t pre_row = 0;
+      typename std::conditional<PAGED, int64_t, int32_t>::type pre_row = 0;
       for (int c = rs.c0; c < rs.c1 && ok; ++c, ++g) {
         const int slot = g & 1;
         const uint32_t fpar = ((g >> 1) & 1) ^ 1;     // completion of PV(g - 2), which read this slot
@@ -434,11 +551,25 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         // Partial blocks of caches, whose tail rows may be unwritten, take the
         // zero-filling path instead.
         const bool fullh = (cl + 1) * kRows <= nset;
-        const bool tma = win ? (p.tma_tok != 0 && (p.src2 == SRC2_WINDOW || fullh))
-                             : (rs.idx == nullptr && p.tma_kv != 0 && fullh);
+        // Paged rows: blocks that start on a multiple of 64 rows lie within one
+        // page of 64 rows or more; a missing page is left to the other path.
+        bool tma;
+        int32_t y0 = 0;
+        if constexpr (PAGED) {
+          const int64_t r0 = (win ? rs.lo2 : 0) + (int64_t)cl * kRows;
+          tma = fullh && (r0 & (kRows - 1)) == 0 && (win ? p.tma_tok != 0 : p.tma_kv != 0);
+          if (tma) {
+            const int64_t g0 = page_row(win ? p.pt2 : p.pt1, b, r0);
+            tma = g0 >= 0;
+            y0 = (int32_t)g0;
+          }
+        } else {
+          tma = win ? (p.tma_tok != 0 && (p.src2 == SRC2_WINDOW || fullh))
+                    : (rs.idx == nullptr && p.tma_kv != 0 && fullh);
+          y0 = win ? (int32_t)((int64_t)b * p.cap2 + rs.lo2 + (int64_t)cl * kRows)
+                   : (int32_t)((int64_t)b * p.cap + (int64_t)cl * kRows);
+        }
         if (tma) {
-          const int32_t y0 = win ? (int32_t)((int64_t)b * p.cap2 + rs.lo2 + (int64_t)cl * kRows)
-                                 : (int32_t)((int64_t)b * p.cap + (int64_t)cl * kRows);
           for (int tt = 0; tt < NT; ++tt) {
             if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
             if (lt == 0) {
@@ -468,8 +599,14 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
               row = r;
             }
           }
-          const uint8_t* rp = win ? reinterpret_cast<const uint8_t*>(p.kv2) + ((int64_t)b * p.cap2 + row) * D * 2
-                                  : reinterpret_cast<const uint8_t*>(p.kv) + ((int64_t)b * p.cap + row) * D * 2;
+          if constexpr (PAGED) {
+            // a row without a page is recorded and read as zeros
+            if (valid) row = page_row(win ? p.pt2 : p.pt1, b, row);
+            if (row < 0) { atomicOr(&g_err_attn, DEV_ERR_BAD_INDEX); valid = false; row = 0; }
+          } else {
+            row += win ? (int64_t)b * p.cap2 : (int64_t)b * p.cap;
+          }
+          const uint8_t* rp = reinterpret_cast<const uint8_t*>(win ? p.kv2 : p.kv) + row * D * 2;
           // Slab pair tt is signalled once this thread's copies of it have landed
           // (cp.async group tt), fenced to the async proxy here, on the producer
           // side, so the MMA issuer needs no proxy fence of its own.
@@ -510,7 +647,12 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
             const int r1 = (cc - rs.nh2) * kRows + 16 * lw + rl;
             bool vld = r1 < rs.n1;
             int64_t row1 = 0;
-            if (vld) {
+            if constexpr (PAGED) {
+              if (vld) {
+                row1 = pre_c == cc ? pre_row : page_row(p.pt1, b, r1);
+                if (row1 < 0) { atomicOr(&g_err_attn, DEV_ERR_BAD_INDEX); vld = false; row1 = 0; }
+              }
+            } else if (vld) {
               if (rs.idx) {
                 row1 = pre_c == cc ? pre_row : __ldg(rs.idx + r1);
                 if (row1 < 0 || row1 >= p.cap) { atomicOr(&g_err_attn, DEV_ERR_BAD_INDEX); vld = false; row1 = 0; }
@@ -518,7 +660,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
                 row1 = r1;
               }
             }
-            const long long gr0 = (long long)b * p.cap + row1;
+            const long long gr0 = PAGED ? row1 : (long long)b * p.cap + row1;
             scv = vld ? __ldg(p.kv_scale + gr0) : 0.f;
             const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -551,7 +693,17 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           if (c + 1 < rs.c1) {
             const int r0 = (c + 1 - rs.nh2) * kRows;
             const int nr = min(kRows, rs.n1 - r0);
-            if (rs.idx == nullptr) {
+            if constexpr (PAGED) {
+              // the next half chunk's rows, looked up ahead; each row's bytes into L2
+              if (16 * lw + rl < nr) {
+                pre_row = page_row(p.pt1, b, r0 + 16 * lw + rl);
+                pre_c = c + 1;
+                if (lane < 16 && pre_row >= 0) {
+                  prefetch_l2_bulk(kvn + (long long)pre_row * kNope, kNope);
+                  prefetch_l2_bulk(kvr + (long long)pre_row * 128, 128);
+                }
+              }
+            } else if (rs.idx == nullptr) {
               const long long g0 = (long long)b * p.cap + r0;
               if (lt == 0) prefetch_l2_bulk(kvn + g0 * kNope, (uint32_t)(nr * kNope));
               else if (lt == 1) prefetch_l2_bulk(kvr + g0 * 128, (uint32_t)(nr * 128));
@@ -685,10 +837,10 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     for (uint32_t kk = 0; ok; ++kk) {
       const int64_t item = get_item(kk, false);
       if (item >= n_items) break;
-      const int64_t bt = item / p.n_split;
-      const int sp = (int)(item % p.n_split);
-      const int b = (int)(bt / p.T), t = (int)(bt % p.T);
-      const RowSet rs = row_set_warp(p, b, t, sp, lane);
+      Item it;
+      if (!locate_warp<PAGED>(p, plan, item, lane, it)) continue;
+      const int b = it.b, t = it.t;
+      const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per);
       if (rs.c1 <= rs.c0) continue;
       if (lane == 0) {
         if (role == 1) {
@@ -738,10 +890,11 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     for (uint32_t kk = 0; ok; ++kk) {
       const int64_t item = get_item(kk, false);
       if (item >= n_items) break;
-      const int64_t bt = item / p.n_split;
-      const int sp = (int)(item % p.n_split);
-      const int b = (int)(bt / p.T), t = (int)(bt % p.T);
-      const RowSet rs = row_set_warp(p, b, t, sp, lane);
+      Item it;
+      if (!locate_warp<PAGED>(p, plan, item, lane, it)) continue;
+      const int b = it.b, t = it.t;
+      const int64_t bt = it.bt;
+      const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per);
       const int64_t pos = (p.q_pos ? p.q_pos[b] : 0) + t;
       float2* cs = s_cs + (icount & 1) * 32;
       if (EPI == EPI_COMBINE && p.inv_rope && tid < 32) {
@@ -892,20 +1045,22 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       for (int j = 0; j < 2; ++j) {
         const int col = 2 * lane + j;
         const float lt = red[col] + red[64 + col] + red[128 + col] + red[192 + col];
-        const float lse_w = (lt > 0.f) ? (m_own[j] + log2f(lt)) * kLn2 : -CUDART_INF_F;
+        // a paged call passes a NaN on (a visible row holds one) instead of dropping the range
+        const bool some = PAGED ? lt != 0.f : lt > 0.f;
+        const float lse_w = some ? (m_own[j] + log2f(lt)) * kLn2 : -CUDART_INF_F;
         float cw, cp = 0.f;
         if (EPI == EPI_PARTIAL) {
-          cw = lt > 0.f ? 1.f / lt : 0.f;
-          if (warp == 0 && col < p.H) p.lse_part[(bt * p.n_split + sp) * p.H + col] = lse_w;
+          cw = some ? 1.f / lt : 0.f;
+          if (warp == 0 && col < p.H) p.lse_part[item * p.H + col] = lse_w;
         } else {
-          const int64_t o = ((int64_t)b * p.T + t) * p.H + (col < p.H ? col : 0);
+          const int64_t o = bt * p.H + (col < p.H ? col : 0);
           const float lse_p = (p.O_in && col < p.H) ? p.lse_in[o] : -CUDART_INF_F;
           const float sk = (p.sink && col < p.H) ? p.sink[col] : -CUDART_INF_F;
           float M = fmaxf(fmaxf(lse_w, lse_p), sk);
           if (M == -CUDART_INF_F) M = 0.f;
           const float ew = __expf(lse_w - M), ep = __expf(lse_p - M), es = __expf(sk - M);
           const float den = ew + ep + es;
-          cw = lt > 0.f ? ew / (den * lt) : 0.f;
+          cw = some ? ew / (den * lt) : 0.f;
           cp = den > 0.f ? ep / den : 0.f;
         }
         bc_m[64 + col] = cw;
@@ -923,12 +1078,13 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       // writes them straight out (a warp covers 32 consecutive d of one head per
       // store).  The RoPE dims pair d with d +- 32, held by the other warp of the
       // last tile's upper half: those 64 threads exchange through shared memory.
-      const int64_t obase = (bt * p.n_split + sp) * p.H;   // n_split = 1: token row
+      // row of the partial results, or the token's row
+      const int64_t obase = (EPI == EPI_PARTIAL ? item : bt) * p.H;
       float* xs = reinterpret_cast<float*>(sP);            // [64 heads][64 lanes] exchange
       // an empty range of a split token leaves its partial output unwritten: its
       // lse is -inf and the merge does not read it (a plain partial call still
       // writes O = 0 for an empty row set)
-      const int n_out_tiles = (EPI == EPI_PARTIAL && !any && p.per_item > 0) ? 0 : NT;
+      const int n_out_tiles = (EPI == EPI_PARTIAL && !any && (PAGED || p.per_item > 0)) ? 0 : NT;
       for (int tt = 0; tt < n_out_tiles; ++tt) {
         float o[64];
         if (any) {
@@ -1110,6 +1266,72 @@ attn_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, co
       dst[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
   }
+}
+
+// Merge of a paged call's ranges: the partial results of a token (O normalised
+// by its own sum, lse) and the sink in one softmax.  A warp takes 128 dims of
+// one head of one token, 16 bytes a lane, four partials in flight; it skips
+// empty ranges, whose output was not written.
+__global__ void __launch_bounds__(128)
+paged_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, const int32_t* __restrict__ plan,
+                   const float* __restrict__ sink, const int32_t* __restrict__ cu_q, int n_seq, int max_items, int H,
+                   int D, void* __restrict__ out, int out_bf16) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int unit = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int per_head = D / 128;
+  const int h = unit / per_head, d = (unit % per_head) * 128 + 4 * lane;
+  const int64_t bt = blockIdx.x;
+  const int b = find_seq_warp(cu_q, n_seq, bt, lane);
+  if (b < 0 || h >= H) return;
+  const int c0 = cu_q[b], f0 = plan[b];
+  const int ns = (plan[b + 1] - f0) / (cu_q[b + 1] - c0);
+  const int64_t i0 = f0 + (bt - c0) * ns;
+  if (i0 + ns > max_items) return;
+  const float sk = sink ? sink[h] : -CUDART_INF_F;
+  float M = sk;
+  for (int i = lane; i < ns; i += 32) M = fmaxf(M, Ls[(i0 + i) * H + h]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (M == -CUDART_INF_F) M = 0.f;
+  float den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < ns; s0 += 32) {
+    const int s = s0 + lane;
+    const float e = s < ns ? __expf(Ls[(i0 + s) * H + h] - M) : 0.f;
+    den += e;
+    const int n = min(32, ns - s0);
+    for (int j0 = 0; j0 < n; j0 += 4) {
+      float c[4];
+      float4 a[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        c[u] = __shfl_sync(0xffffffffu, e, (j0 + u) & 31);
+        const bool in = j0 + u < n && c[u] != 0.f;        // NaN reads too
+        if (!in) c[u] = 0.f;
+        a[u] = in ? __ldg(reinterpret_cast<const float4*>(Os + ((i0 + s0 + j0 + u) * H + h) * D + d))
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        acc.x = fmaf(c[u], a[u].x, acc.x);
+        acc.y = fmaf(c[u], a[u].y, acc.y);
+        acc.z = fmaf(c[u], a[u].z, acc.z);
+        acc.w = fmaf(c[u], a[u].w, acc.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  if (sink) den += __expf(sk - M);
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const int64_t o = (bt * H + h) * (int64_t)D + d;
+  if (out_bf16)
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + o) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  else
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + o) =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
 // ---------------------------------------------------------------------------
@@ -1301,6 +1523,28 @@ csa_status_t launch_attn(const AttnParams& p, const AttnMaps& m, cudaStream_t st
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p, m.q, m.kv, m.tok);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "attention: launch failed: %s", cudaGetErrorString(e));
   return check_launch("attention");
+}
+
+template <int D, int KV, int EPI>
+csa_status_t launch_paged(const AttnParams& p, const AttnMaps& m, cudaStream_t st) {
+  constexpr int NS = D / 64, NT = D / 128;
+  const size_t smem = 1024 + NS * (kNQ * 128) + 2 * NS * (kRows * 128) + 2 * (kRows * 128) +
+                      (2 * 4 * 64 + 4 * 3 * 64) * 4 + 64 * 8 + (9 + 4 * NT + 8) * 8 + 4 * 8 + 16 +
+                      (EPI == EPI_PARTIAL ? sizeof(SplitPlan) : 0);
+  auto kern = attn_kernel<D, KV, EPI, true>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
+  const int grid = EPI == EPI_PARTIAL ? std::min(p.max_items, num_sms()) : (int)std::min<int64_t>(p.n_tok, num_sms());
+  e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p, m.q, m.kv, m.tok);
+  if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: launch failed: %s", cudaGetErrorString(e));
+  return check_launch("csa_paged_attention");
+}
+
+template <int EPI>
+csa_status_t dispatch_paged(const AttnParams& p, const AttnMaps& m, int D, csa_dtype_t kv_dtype, cudaStream_t st) {
+  if (D == 512)
+    return kv_dtype == CSA_E4M3 ? launch_paged<512, KV_FP8, EPI>(p, m, st) : launch_paged<512, KV_BF16, EPI>(p, m, st);
+  return kv_dtype == CSA_E4M3 ? launch_paged<128, KV_FP8, EPI>(p, m, st) : launch_paged<128, KV_BF16, EPI>(p, m, st);
 }
 
 // Builds the tile maps that apply (bf16 rows, 64 x 64-row boxes, 128-byte
@@ -1532,4 +1776,117 @@ extern "C" csa_status_t csa_fused_attention_splitkv(const void* q, csa_dtype_t q
   if (le != cudaSuccess)
     return fail(CSA_ERR_CUDA, "csa_fused_attention_splitkv(merge): launch failed: %s", cudaGetErrorString(le));
   return check_launch("csa_fused_attention_splitkv(merge)");
+}
+
+namespace {
+
+// Ranges that a paged call is cut into, 0 if it is not: with few query tokens
+// (at most half the SMs) the tokens alone leave SMs idle, so their row sets are
+// cut to give every SM one range.
+int paged_items(int64_t n_tok, int n_seq) {
+  const int sms = num_sms();
+  return n_tok * 2 <= sms && n_seq <= kPlanSeqs ? sms : 0;
+}
+
+csa_status_t check_pages(const char* what, const void* pages, const int32_t* table, int max_pages, int64_t n_pages,
+                         int page_size) {
+  CSA_REQUIRE(aligned16(pages), "csa_paged_attention: %s pages must be 16-byte aligned", what);
+  CSA_REQUIRE(table && reinterpret_cast<uintptr_t>(table) % 4 == 0, "csa_paged_attention: %s table required", what);
+  CSA_REQUIRE(max_pages >= 1 && n_pages >= 1, "csa_paged_attention: %s max_pages and n_pages must be positive", what);
+  CSA_REQUIRE(page_size >= 1 && page_size <= 65536 && (page_size & (page_size - 1)) == 0,
+              "csa_paged_attention: %s page_size must be a power of two, at most 65536", what);
+  if ((int64_t)max_pages * page_size >= (int64_t)1 << 31)
+    return fail(CSA_ERR_UNSUPPORTED, "csa_paged_attention: a sequence may have at most 2^31 - 1 %s rows", what);
+  return CSA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t csa_paged_attention_workspace(int64_t n_tok, int n_seq, int H, int D) {
+  if (n_tok <= 0 || n_seq <= 0 || H <= 0 || D <= 0) return 0;
+  const size_t items = (size_t)paged_items(n_tok, n_seq);
+  if (items == 0) return 0;
+  // the ranges' results, their lse, the first range of each sequence
+  return ((items * H * D * 4 + 255) / 256) * 256 + ((items * H * 4 + 255) / 256) * 256 + (((size_t)n_seq + 1) * 4 + 255) / 256 * 256;
+}
+
+extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H, int D, const int32_t* cu_q,
+                                            const int64_t* q_pos, int n_seq, const void* tok_pages,
+                                            const int32_t* tok_table, int tok_max_pages, int64_t n_tok_pages,
+                                            int tok_page_size, int W, const void* kv_pages, csa_dtype_t kv_dtype,
+                                            const void* kv_rope, const float* kv_scale, const int32_t* kv_table,
+                                            int kv_max_pages, int64_t n_kv_pages, int kv_page_size, int m,
+                                            const float* sink, float scale, void* workspace, size_t ws_bytes, void* out,
+                                            csa_dtype_t out_dtype, cudaStream_t stream) {
+  clear_error();
+  CSA_REQUIRE(n_tok >= 0 && n_seq >= 0, "csa_paged_attention: n_tok and n_seq must not be negative");
+  CSA_REQUIRE(H >= 1 && H <= 64, "csa_paged_attention: H must be in [1, 64]");
+  CSA_REQUIRE(D == 128 || D == 512, "csa_paged_attention: D must be 128 or 512");
+  CSA_REQUIRE(out_dtype == CSA_F32 || out_dtype == CSA_BF16, "csa_paged_attention: out_dtype must be F32 or BF16");
+  CSA_REQUIRE(tok_pages || kv_pages, "csa_paged_attention: token pages or entry pages required");
+  CSA_REQUIRE(W >= 0, "csa_paged_attention: W must not be negative");
+  if (n_tok == 0 || n_seq == 0) return CSA_OK;
+  if (n_tok * H >= (int64_t)1 << 31) return fail(CSA_ERR_UNSUPPORTED, "csa_paged_attention: n_tok * H must be below 2^31");
+  CSA_REQUIRE(q && out && aligned16(q) && aligned16(out), "csa_paged_attention: q / out must be non-null and 16-byte aligned");
+  CSA_REQUIRE(cu_q && q_pos && reinterpret_cast<uintptr_t>(cu_q) % 4 == 0 && reinterpret_cast<uintptr_t>(q_pos) % 8 == 0,
+              "csa_paged_attention: cu_q and q_pos required, aligned to their elements");
+  csa_status_t s;
+  AttnParams p{};
+  if (tok_pages) {
+    s = check_pages("token", tok_pages, tok_table, tok_max_pages, n_tok_pages, tok_page_size);
+    if (s != CSA_OK) return s;
+    p.kv2 = tok_pages; p.src2 = SRC2_WINDOW; p.W = W; p.cap2 = (int64_t)tok_max_pages * tok_page_size;
+    p.pt2 = PageTable{tok_table, n_tok_pages, tok_max_pages, __builtin_ctz((unsigned)tok_page_size)};
+  }
+  if (kv_pages) {
+    CSA_REQUIRE(kv_dtype == CSA_BF16 || kv_dtype == CSA_E4M3, "csa_paged_attention: kv_dtype must be BF16 or E4M3");
+    CSA_REQUIRE(m >= 1, "csa_paged_attention: m must be positive");
+    s = check_pages("entry", kv_pages, kv_table, kv_max_pages, n_kv_pages, kv_page_size);
+    if (s != CSA_OK) return s;
+    CSA_REQUIRE(kv_dtype != CSA_E4M3 || (kv_rope && kv_scale && aligned16(kv_rope) && aligned16(kv_scale)),
+                "csa_paged_attention: e4m3 entries need kv_rope and kv_scale, 16-byte aligned");
+    p.kv = kv_pages; p.kv_rope = (const __nv_bfloat16*)kv_rope; p.kv_scale = kv_scale;
+    p.src1 = SRC1_DENSE; p.m = m; p.cap = (int64_t)kv_max_pages * kv_page_size;
+    p.pt1 = PageTable{kv_table, n_kv_pages, kv_max_pages, __builtin_ctz((unsigned)kv_page_size)};
+  } else {
+    kv_dtype = CSA_BF16;
+    p.m = 1;
+  }
+  p.q = q; p.q_pos = q_pos; p.cu_q = cu_q; p.n_tok = n_tok; p.n_seq = n_seq; p.T = 1; p.H = H; p.n_split = 1;
+  p.scale = scale; p.scale_log2 = scale * 1.4426950408889634f;
+  p.sink = sink; p.out = out; p.out_bf16 = out_dtype == CSA_BF16;
+  AttnMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (!encode_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, D, n_tok * H, 64, kNQ, CU_TENSOR_MAP_SWIZZLE_128B))
+    return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (queries) failed");
+  p.tma_q = 1;
+  // blocks of 64 rows lie within one page from 64 rows a page on
+  if (p.src1 == SRC1_DENSE && kv_dtype == CSA_BF16 && kv_page_size >= kRows && n_kv_pages * kv_page_size < (int64_t)1 << 31) {
+    if (!encode_2d(&maps.kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_pages, D, n_kv_pages * kv_page_size, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
+      return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (entries) failed");
+    p.tma_kv = 1;
+  }
+  if (p.src2 == SRC2_WINDOW && tok_page_size >= kRows && n_tok_pages * tok_page_size < (int64_t)1 << 31) {
+    if (!encode_2d(&maps.tok, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, tok_pages, D, n_tok_pages * tok_page_size, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
+      return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (tokens) failed");
+    p.tma_tok = 1;
+  }
+  p.max_items = paged_items(n_tok, n_seq);
+  if (p.max_items == 0) return dispatch_paged<EPI_COMBINE>(p, maps, D, kv_dtype, stream);
+  const size_t need = csa_paged_attention_workspace(n_tok, n_seq, H, D);
+  if (!workspace || ws_bytes < need)
+    return fail(CSA_ERR_WORKSPACE, "csa_paged_attention: workspace of %zu bytes needed, %zu given", need, ws_bytes);
+  CSA_REQUIRE(aligned16(workspace), "csa_paged_attention: workspace must be 16-byte aligned");
+  const size_t items = (size_t)p.max_items;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.O_part = reinterpret_cast<float*>(ws);
+  p.lse_part = reinterpret_cast<float*>(ws + ((items * H * D * 4 + 255) / 256) * 256);
+  p.plan = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(p.lse_part) + ((items * H * 4 + 255) / 256) * 256);
+  s = dispatch_paged<EPI_PARTIAL>(p, maps, D, kv_dtype, stream);
+  if (s != CSA_OK) return s;
+  cudaError_t le = launch_pdl(paged_merge_kernel, dim3((unsigned)n_tok, (unsigned)((H * (D / 128) + 3) / 4)), dim3(128), 0,
+                              stream, (const float*)p.O_part, (const float*)p.lse_part, (const int32_t*)p.plan, sink, cu_q,
+                              n_seq, p.max_items, H, D, out, (int)p.out_bf16);
+  if (le != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention(merge): launch failed: %s", cudaGetErrorString(le));
+  return check_launch("csa_paged_attention(merge)");
 }

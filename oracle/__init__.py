@@ -8,3 +8,6 @@ See ``oracle/csa_oracle.py`` for the functions and the passages they follow.
 """
 from .csa_oracle import *  # noqa: F401,F403
 from .csa_oracle import __all__  # noqa: F401
+from .paged_oracle import *  # noqa: F401,F403,E402
+from .paged_oracle import __all__ as _paged  # noqa: E402
+__all__ = list(__all__) + list(_paged)
