@@ -18,6 +18,7 @@ paged_layer_step.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -390,81 +391,96 @@ def csa_grouped_out_proj(o, w_grp, w_out, *, mid=None, out=None, out_dtype=torch
 
 # ---------------------------------------------------------------- paged serving step
 
-def _batch_args(what, dev, cu_q, q_pos, **tensors):
-    """Checks what the paged calls share: every tensor on device `dev`, cu_q
-    [n_seq + 1] int32 and q_pos [n_seq] int64.  Returns n_seq."""
-    for n, t in dict(cu_q=cu_q, q_pos=q_pos, **tensors).items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise CsaError(f"{what}: {n} must be a CUDA tensor")
-        if t.device != dev:
-            raise CsaError(f"{what}: {n} is on {t.device}, not {dev}")
-    if cu_q.dtype != torch.int32 or q_pos.dtype != torch.int64 or q_pos.dim() != 1 or \
-            tuple(cu_q.shape) != (q_pos.shape[0] + 1,) or not (cu_q.is_contiguous() and q_pos.is_contiguous()):
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _batch(what, cu_q, q_pos, tensors):
+    """Checks what the paged calls share: every tensor (None: absent) on one
+    CUDA device, cu_q [n_seq + 1] int32 and q_pos [n_seq] int64.  Returns
+    (device index, n_seq).  These calls are short on the device, so the checks
+    keep to plain attribute reads."""
+    dev = tensors[0].get_device()
+    if dev < 0 or cu_q.get_device() != dev or q_pos.get_device() != dev:
+        raise CsaError(f"{what}: every tensor must be a CUDA tensor of one device")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise CsaError(f"{what}: every tensor must be a CUDA tensor of one device")
+    n = q_pos.shape
+    if cu_q.dtype is not torch.int32 or q_pos.dtype is not torch.int64 or len(n) != 1 or \
+            cu_q.shape != (n[0] + 1,) or not (cu_q.is_contiguous() and q_pos.is_contiguous()):
         raise CsaError(f"{what}: cu_q [n_seq + 1] int32 and q_pos [n_seq] int64, contiguous, expected")
-    return q_pos.shape[0]
+    return dev, n[0]
 
 
-class _on:
-    """Makes a tensor's device current, and on it the given stream (else that
-    device's current one), so that what a call allocates belongs to the stream
-    that it launches on.  Yields the stream handle."""
+class _Elsewhere:
+    """Makes a device current, and on it the given stream (else that device's
+    current one), so that what a call allocates belongs to the stream that it
+    launches on."""
 
     def __init__(self, dev, stream):
-        self.dev = torch.cuda.device(dev)
-        self.stream = stream
+        self.ctx = [torch.cuda.device(dev)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
-        self.dev.__enter__()
-        if self.stream is None:
-            self.ctx = None
-            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        self.ctx = torch.cuda.stream(self.stream)
-        self.ctx.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        for c in self.ctx:
+            c.__enter__()
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        self.dev.__exit__(*exc)
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
 
 
-def _float_dtype(what, name, t):
-    if t.dtype not in (torch.float32, torch.bfloat16):
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(what, dev, stream):
+    """The context of a call on `dev`: nothing to do on the current device and stream."""
+    if stream is None and dev == torch._C._cuda_getDevice():
+        return _HERE_ALREADY
+    if stream is not None and stream.device_index != dev:
+        raise CsaError(f"{what}: the stream and the tensors are on different devices")
+    return _Elsewhere(dev, stream)
+
+
+def _heads(what, name, t):
+    """(n, H, D, token stride, head stride) of rows [n, H, D] or [n, D]."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
         raise CsaError(f"{what}: {name} must be float32 or bfloat16")
-
-
-def _heads(what, name, t, out=False):
-    """(t as [n, H, D], token stride, head stride) of rows [n, H, D] or [n, D]."""
-    if t.dim() == 2:
-        t = t.unsqueeze(1)
-    if t.dim() != 3:
+    if len(shape) == 3:
+        (n, H, D), (ts, hs, ds) = shape, stride
+    elif len(shape) == 2:
+        (n, D), (ts, ds), H, hs = shape, stride, 1, 0
+    else:
         raise CsaError(f"{what}: {name} must be [n_tok, H, D] or [n_tok, D]")
-    _float_dtype(what, name, t)
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if ds != 1 and D > 1:
         raise CsaError(f"{what}: the last dimension of {name} must be contiguous")
-    ts = t.stride(0) if t.shape[0] > 1 else 0
-    hs = t.stride(1) if t.shape[1] > 1 else 0
-    if out and t.numel():
-        D = t.shape[2]
-        used = sorted((s, n) for s, n in ((ts, t.shape[0]), (hs, t.shape[1])) if n > 1)
-        if used and (used[0][0] < D or (len(used) == 2 and used[1][0] < used[0][0] * (used[0][1] - 1) + D)):
-            raise CsaError(f"{what}: the rows of {name} overlap")
-    return t, ts, hs
+    return n, H, D, ts if n > 1 else 0, hs if H > 1 else 0
+
+
+def _out_heads(what, name, t):
+    """_heads of an output: its rows may not overlap."""
+    n, H, D, ts, hs = r = _heads(what, name, t)
+    used = sorted((s, k) for s, k in ((ts, n), (hs, H)) if k > 1)
+    if n and H and used and (used[0][0] < D or (len(used) == 2 and used[1][0] < used[0][0] * (used[0][1] - 1) + D)):
+        raise CsaError(f"{what}: the rows of {name} overlap")
+    return r
 
 
 def _freqs(what, inv_freq):
     if inv_freq is None:
         return 0
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise CsaError(f"{what}: inv_freq must be a contiguous float64 [rope_dim / 2]")
     return 2 * inv_freq.shape[0]
 
 
-def _gain(what, name, g, D):
-    if g is not None and (g.dtype != torch.float32 or tuple(g.shape) != (D,) or not g.is_contiguous()):
-        raise CsaError(f"{what}: {name} must be a contiguous float32 [{D}]")
+def _vector(what, name, g, n):
+    if g is not None and (g.dtype is not torch.float32 or g.shape != (n,) or not g.is_contiguous()):
+        raise CsaError(f"{what}: {name} must be a contiguous float32 [{n}]")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _shares(a, b):
@@ -488,6 +504,15 @@ def _shares(a, b):
     return True
 
 
+def _same_start(a, b):
+    return a.data_ptr() == b.data_ptr() and a.numel() > 0 and b.numel() > 0
+
+
+def _overlap(a, b):
+    """Whether two tensors share memory, the same view included."""
+    return _same_start(a, b) or _shares(a, b)
+
+
 def csa_rope_freqs(rope_dim, *, base=10000.0, factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0,
                    device="cuda"):
     """Frequencies of the rotation, (inv_freq [rope_dim / 2] float64 on `device`,
@@ -508,21 +533,24 @@ def csa_rope(x, cu_q, q_pos, inv_freq, *, rope_start=None, interleaved=False, in
     rope_start (default: the last rope_dim elements) turn by position *
     inv_freq and scale by mscale.  out=x rotates in place."""
     what = "csa_rope"
-    n_seq = _batch_args(what, x.device, cu_q, q_pos, x=x, inv_freq=inv_freq, out=out)
-    x3, xt, xh = _heads(what, "x", x)
+    dev, n_seq = _batch(what, cu_q, q_pos, (x, inv_freq, out))
+    n, H, D, xt, xh = _heads(what, "x", x)
     r = _freqs(what, inv_freq)
-    n, H, D = x3.shape
-    with _on(x.device, stream) as st:
+    with _on(what, dev, stream):
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-        elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
-            raise CsaError(f"{what}: out must have x's shape and out_dtype")
-        o3, ot, oh = _heads(what, "out", out, out=True)
-        if _shares(x, out):
-            raise CsaError(f"{what}: out must be x itself or not overlap it")
-        _check(lib().csa_rope(_ptr(x), _DT[x.dtype], xt, xh, n, H, D, _ptr(cu_q), _ptr(q_pos), n_seq, _ptr(inv_freq), r,
-                              D - r if rope_start is None else rope_start, int(interleaved), int(inverse), mscale,
-                              _ptr(out), _DT[out.dtype], ot, oh, st), what)
+            out = x.new_empty(x.shape, dtype=out_dtype)
+            ot, oh = H * D, D
+        else:
+            if out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
+                raise CsaError(f"{what}: out must have x's shape and out_dtype")
+            _, _, _, ot, oh = _out_heads(what, "out", out)
+            if out is x:
+                ot, oh = xt, xh
+            elif _shares(x, out):
+                raise CsaError(f"{what}: out must be x itself or not overlap it")
+        _check(lib().csa_rope(x.data_ptr(), _DT[x.dtype], xt, xh, n, H, D, cu_q.data_ptr(), q_pos.data_ptr(), n_seq,
+                              _at(inv_freq), r, D - r if rope_start is None else rope_start, interleaved, inverse,
+                              mscale, out.data_ptr(), _DT[out.dtype], ot, oh, _raw_stream(dev)), what)
     return out
 
 
@@ -533,56 +561,70 @@ def csa_qk_norm_rope(q, k, cu_q, q_pos, inv_freq, *, q_gain=None, k_gain=None, r
     launch; views of one projection's output are read in place.  Returns
     (q_out, k_out)."""
     what = "csa_qk_norm_rope"
-    n_seq = _batch_args(what, q.device, cu_q, q_pos, q=q, k=k, inv_freq=inv_freq, q_gain=q_gain, k_gain=k_gain,
-                        q_out=q_out, k_out=k_out)
+    dev, n_seq = _batch(what, cu_q, q_pos, (q, k, inv_freq, q_gain, k_gain, q_out, k_out))
     r = _freqs(what, inv_freq)
-    q3, qt, qh = _heads(what, "q", q)
-    n, H, D = q3.shape
-    _gain(what, "q_gain", q_gain, D)
-    _gain(what, "k_gain", k_gain, D)
-    with _on(q.device, stream) as st:
-        outs = []
-        for name, x, o in (("q", q, q_out), ("k", k, k_out)):
-            if x is None:
-                if o is not None:
-                    raise CsaError(f"{what}: {name}_out without {name}")
-                outs.append((None, 0, 0, None, 0, 0, 0))
-                continue
-            x3, xt, xh = _heads(what, name, x)
-            if x3.shape[0] != n or x3.shape[2] != D or x.dtype != q.dtype:
-                raise CsaError(f"{what}: q [n_tok, H, D] and k [n_tok, Hk, D] of one dtype expected")
-            if o is None:
-                o = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-            elif o.shape != x.shape or (out_dtype is not None and o.dtype != out_dtype):
-                raise CsaError(f"{what}: {name}_out must have the shape of {name} and out_dtype")
-            _, ot, oh = _heads(what, name + "_out", o, out=True)
-            outs.append((x, xt, xh, o, ot, oh, x3.shape[1]))
-        (_, qt, qh, qo, qot, qoh, H), (_, kt, kh, ko, kot, koh, Hk) = outs
-        if ko is not None and ko.dtype != qo.dtype:
-            raise CsaError(f"{what}: the outputs must have one dtype")
-        for o in (qo, ko):
-            for x in (q, k):
-                if o is not None and x is not None and _shares(x, o):
-                    raise CsaError(f"{what}: an output must be its input itself or overlap neither input")
-        if ko is not None and (_shares(qo, ko) or (qo.data_ptr() == ko.data_ptr() and qo.numel() > 0)):
-            raise CsaError(f"{what}: the outputs overlap")
-        _check(lib().csa_qk_norm_rope(_ptr(q), qt, qh, H, _ptr(k), kt, kh, Hk, _DT[q.dtype], n, D, _ptr(cu_q),
-                                      _ptr(q_pos), n_seq, _ptr(q_gain), _ptr(k_gain), eps, _ptr(inv_freq), r,
-                                      D - r if rope_start is None else rope_start, int(interleaved), mscale, _ptr(qo),
-                                      qot, qoh, _ptr(ko), kot, koh, _DT[qo.dtype], st), what)
-    return qo, ko
+    n, H, D, qt, qh = _heads(what, "q", q)
+    _vector(what, "q_gain", q_gain, D)
+    _vector(what, "k_gain", k_gain, D)
+    if k is None:
+        if k_out is not None:
+            raise CsaError(f"{what}: k_out without k")
+        Hk = kt = kh = 0
+    else:
+        nk, Hk, Dk, kt, kh = _heads(what, "k", k)
+        if nk != n or Dk != D or k.dtype is not q.dtype:
+            raise CsaError(f"{what}: q [n_tok, H, D] and k [n_tok, Hk, D] of one dtype expected")
+    given = q_out is not None or k_out is not None
+    qot = H * D
+    qoh = koh = D
+    kot = Hk * D
+    with _on(what, dev, stream):
+        if q_out is None:
+            q_out = q.new_empty(q.shape, dtype=out_dtype)
+        else:
+            _, _, _, qot, qoh = _out_heads(what, "q_out", q_out)
+        if k is None:
+            pass
+        elif k_out is None:
+            k_out = k.new_empty(k.shape, dtype=out_dtype)
+        else:
+            _, _, _, kot, koh = _out_heads(what, "k_out", k_out)
+        if given:
+            for name, x, o in (("q", q, q_out), ("k", k, k_out)):
+                if o is not None and (o.shape != x.shape or (out_dtype is not None and o.dtype != out_dtype)):
+                    raise CsaError(f"{what}: {name}_out must have the shape of {name} and out_dtype")
+            if k is not None and k_out.dtype != q_out.dtype:
+                raise CsaError(f"{what}: the outputs must have one dtype")
+            for o, own, other in ((q_out, q, k), (k_out, k, q)):
+                if o is None:
+                    continue
+                if _shares(own, o) or (other is not None and (_shares(other, o) or _same_start(other, o))):
+                    raise CsaError(f"{what}: an output must be its own input or overlap neither input")
+            if k is not None and (_shares(q_out, k_out) or _same_start(q_out, k_out)):
+                raise CsaError(f"{what}: the outputs overlap")
+            if q_out.data_ptr() == q.data_ptr():
+                qot, qoh = qt, qh
+            if k is not None and k_out.data_ptr() == k.data_ptr():
+                kot, koh = kt, kh
+        _check(lib().csa_qk_norm_rope(q.data_ptr(), qt, qh, H, _at(k), kt, kh, Hk, _DT[q.dtype], n, D, cu_q.data_ptr(),
+                                      q_pos.data_ptr(), n_seq, _at(q_gain), _at(k_gain), eps, _at(inv_freq), r,
+                                      D - r if rope_start is None else rope_start, interleaved, mscale,
+                                      q_out.data_ptr(), qot, qoh, _at(k_out), kot, koh, _DT[q_out.dtype],
+                                      _raw_stream(dev)), what)
+    return q_out, k_out
 
 
 def _table(what, name, table, n_seq):
-    if table is None or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_seq or \
+    if table is None or table.dtype is not torch.int32 or table.dim() != 2 or table.shape[0] != n_seq or \
             not table.is_contiguous():
         raise CsaError(f"{what}: {name} must be a contiguous int32 [n_seq, max_pages]")
 
 
 def _e4m3_pages(what, pages, rope, scale, D):
-    if rope is None or scale is None or rope.dtype != torch.bfloat16 or scale.dtype != torch.float32 or \
-            pages.shape[2] + 64 != D or tuple(rope.shape) != (*pages.shape[:2], 64) or \
-            tuple(scale.shape) != tuple(pages.shape[:2]) or not (rope.is_contiguous() and scale.is_contiguous()):
+    head = pages.shape[:2]
+    if rope is None or scale is None or rope.dtype is not torch.bfloat16 or scale.dtype is not torch.float32 or \
+            pages.shape[2] + 64 != D or rope.shape != (*head, 64) or scale.shape != head or \
+            not (rope.is_contiguous() and scale.is_contiguous()):
         raise CsaError(f"{what}: e4m3 pages are [n_pages, page_size, D - 64] uint8 with [.., 64] bfloat16 and "
                        "[n_pages, page_size] float32")
 
@@ -594,33 +636,32 @@ def csa_paged_append(rows, cu_q, q_pos, block_table, pages, inv_freq, *, pages_r
     bfloat16 or float32, or uint8 e4m3 codes [n_pages, page_size, D - 64] with
     pages_rope [.., 64] bfloat16 and pages_scale [n_pages, page_size] float32."""
     what = "csa_paged_append"
-    n_seq = _batch_args(what, rows.device, cu_q, q_pos, rows=rows, block_table=block_table, pages=pages,
-                        inv_freq=inv_freq, pages_rope=pages_rope, pages_scale=pages_scale, gain=gain)
+    dev, n_seq = _batch(what, cu_q, q_pos, (rows, block_table, pages, inv_freq, pages_rope, pages_scale, gain))
     if rows.dim() != 2:
         raise CsaError(f"{what}: rows must be [n_tok, D]")
-    _, rt, _ = _heads(what, "rows", rows)
-    n, D = rows.shape
+    n, _, D, rt, _ = _heads(what, "rows", rows)
     r = _freqs(what, inv_freq)
-    _gain(what, "gain", gain, D)
+    _vector(what, "gain", gain, D)
     _table(what, "block_table", block_table, n_seq)
-    if pages.dim() != 3 or pages.dtype not in _DT or not pages.is_contiguous():
+    dt = _DT.get(pages.dtype)
+    if pages.dim() != 3 or dt is None or not pages.is_contiguous():
         raise CsaError(f"{what}: pages must be contiguous [n_pages, page_size, D] bfloat16 or float32, or uint8 codes")
-    if pages.dtype == torch.uint8:
+    n_pages, page_size, width = pages.shape
+    if dt == E4M3:
         _e4m3_pages(what, pages, pages_rope, pages_scale, D)
-    elif pages.shape[2] != D or pages_rope is not None or pages_scale is not None:
+    elif width != D or pages_rope is not None or pages_scale is not None:
         raise CsaError(f"{what}: pages [n_pages, page_size, {D}] without rope and scale pages expected")
-    for p in (pages, pages_rope, pages_scale):
-        if p is not None and (_shares(rows, p) or (p.numel() and p.data_ptr() == rows.data_ptr())):
-            raise CsaError(f"{what}: rows and pages overlap")
-    with _on(rows.device, stream) as st:
-        _check(lib().csa_paged_append(_ptr(rows), _DT[rows.dtype], rt, n, D, _ptr(cu_q), _ptr(q_pos), n_seq,
-                                      _ptr(block_table), block_table.shape[1], pages.shape[1], pages.shape[0],
-                                      int(norm), _ptr(gain), eps, _ptr(inv_freq), r, int(interleaved), mscale,
-                                      _ptr(pages), _DT[pages.dtype], _ptr(pages_rope), _ptr(pages_scale), st), what)
+    if _overlap(rows, pages) or (dt == E4M3 and (_overlap(rows, pages_rope) or _overlap(rows, pages_scale))):
+        raise CsaError(f"{what}: rows and pages overlap")
+    with _on(what, dev, stream):
+        _check(lib().csa_paged_append(rows.data_ptr(), _DT[rows.dtype], rt, n, D, cu_q.data_ptr(), q_pos.data_ptr(),
+                                      n_seq, block_table.data_ptr(), block_table.shape[1], page_size, n_pages, norm,
+                                      _at(gain), eps, _at(inv_freq), r, interleaved, mscale, pages.data_ptr(), dt,
+                                      _at(pages_rope), _at(pages_scale), _raw_stream(dev)), what)
 
 
 def csa_paged_attention_workspace(n_tok, n_seq, H, D):
-    return int(lib().csa_paged_attention_workspace(n_tok, n_seq, H, D))
+    return lib().csa_paged_attention_workspace(n_tok, n_seq, H, D)
 
 
 def csa_paged_attention(q, cu_q, q_pos, *, tok_pages=None, tok_table=None, W=128, kv_pages=None, kv_rope=None,
@@ -632,49 +673,59 @@ def csa_paged_attention(q, cu_q, q_pos, *, tok_pages=None, tok_table=None, W=128
     rows (0: all) of tok_pages, with the sink [H] in one softmax.  Either cache
     may be absent.  The tokens' own raw rows are in their pages already."""
     what = "csa_paged_attention"
-    n_seq = _batch_args(what, q.device, cu_q, q_pos, q=q, tok_pages=tok_pages, tok_table=tok_table, kv_pages=kv_pages,
-                        kv_rope=kv_rope, kv_scale=kv_scale, kv_table=kv_table, sink=sink, out=out, workspace=workspace)
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+    dev, n_seq = _batch(what, cu_q, q_pos, (q, tok_pages, tok_table, kv_pages, kv_rope, kv_scale, kv_table, sink, out,
+                                            workspace))
+    shape = q.shape
+    if len(shape) != 3 or q.dtype is not torch.bfloat16 or not q.is_contiguous():
         raise CsaError(f"{what}: q must be a contiguous bfloat16 [n_tok, H, D]")
-    n, H, D = q.shape
+    n, H, D = shape
+    tp = tn = ts = kp = kn = ks = 0
+    kdt = BF16
     if tok_pages is not None:
         _table(what, "tok_table", tok_table, n_seq)
-        if tok_pages.dim() != 3 or tok_pages.dtype != torch.bfloat16 or tok_pages.shape[2] != D or \
+        if tok_pages.dim() != 3 or tok_pages.dtype is not torch.bfloat16 or tok_pages.shape[2] != D or \
                 not tok_pages.is_contiguous():
             raise CsaError(f"{what}: tok_pages must be a contiguous bfloat16 [n_pages, page_size, {D}]")
+        tp = tok_table.shape[1]
+        tn, ts, _ = tok_pages.shape
     if kv_pages is not None:
         _table(what, "kv_table", kv_table, n_seq)
-        if kv_pages.dim() != 3 or not kv_pages.is_contiguous() or kv_pages.dtype not in (torch.bfloat16, torch.uint8):
+        kdt = _DT.get(kv_pages.dtype)
+        if kv_pages.dim() != 3 or not kv_pages.is_contiguous() or kdt not in (BF16, E4M3):
             raise CsaError(f"{what}: kv_pages must be contiguous [n_pages, page_size, D] bfloat16 or uint8 codes")
-        if kv_pages.dtype == torch.uint8:
+        kp = kv_table.shape[1]
+        kn, ks, width = kv_pages.shape
+        if kdt == E4M3:
             _e4m3_pages(what, kv_pages, kv_rope, kv_scale, D)
-        elif kv_pages.shape[2] != D or kv_rope is not None or kv_scale is not None:
+        elif width != D or kv_rope is not None or kv_scale is not None:
             raise CsaError(f"{what}: kv_pages [n_pages, page_size, {D}] without rope and scale pages expected")
-    if sink is not None and (sink.dtype != torch.float32 or tuple(sink.shape) != (H,) or not sink.is_contiguous()):
-        raise CsaError(f"{what}: sink must be a contiguous float32 [{H}]")
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    with _on(q.device, stream) as st:
+    _vector(what, "sink", sink, H)
+    with _on(what, dev, stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
-        if out.shape != q.shape or out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or \
-                (out_dtype is not None and out.dtype != out_dtype):
-            raise CsaError(f"{what}: out must be contiguous, of q's shape, float32 or bfloat16")
-        if any(t is not None and n and (_shares(t, out) or t.data_ptr() == out.data_ptr())
-               for t in (q, tok_pages, kv_pages, kv_rope)):
-            raise CsaError(f"{what}: out overlaps an input")
+            out = q.new_empty(shape, dtype=out_dtype)
+            if out_dtype is not None and out_dtype not in (torch.float32, torch.bfloat16):
+                raise CsaError(f"{what}: out must be float32 or bfloat16")
+        else:
+            if out.shape != shape or out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or \
+                    (out_dtype is not None and out.dtype != out_dtype):
+                raise CsaError(f"{what}: out must be contiguous, of q's shape, float32 or bfloat16")
+            if any(t is not None and _overlap(t, out) for t in (q, tok_pages, kv_pages, kv_rope, kv_scale)):
+                raise CsaError(f"{what}: out overlaps an input")
+        L = lib()
+        ws_bytes = 0
         if workspace is None:
-            need = csa_paged_attention_workspace(n, n_seq, H, D)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        elif not workspace.is_contiguous():
-            raise CsaError(f"{what}: workspace must be contiguous")
-        tp, tn, ts = (tok_table.shape[1], tok_pages.shape[0], tok_pages.shape[1]) if tok_pages is not None else (0, 0, 0)
-        kp, kn, ks = (kv_table.shape[1], kv_pages.shape[0], kv_pages.shape[1]) if kv_pages is not None else (0, 0, 0)
-        _check(lib().csa_paged_attention(
-            _ptr(q), n, H, D, _ptr(cu_q), _ptr(q_pos), n_seq, _ptr(tok_pages), _ptr(tok_table), tp, tn, ts, W,
-            _ptr(kv_pages), BF16 if kv_pages is None else _DT[kv_pages.dtype], _ptr(kv_rope), _ptr(kv_scale),
-            _ptr(kv_table), kp, kn, ks, m, _ptr(sink), scale, _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(out), _DT[out.dtype], st),
-            what)
+            ws_bytes = L.csa_paged_attention_workspace(n, n_seq, H, D)
+            if ws_bytes:
+                workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
+        else:
+            if not workspace.is_contiguous():
+                raise CsaError(f"{what}: workspace must be contiguous")
+            ws_bytes = workspace.numel() * workspace.element_size()
+        _check(L.csa_paged_attention(
+            q.data_ptr(), n, H, D, cu_q.data_ptr(), q_pos.data_ptr(), n_seq, _at(tok_pages), _at(tok_table), tp, tn, ts,
+            W, _at(kv_pages), kdt, _at(kv_rope), _at(kv_scale), _at(kv_table), kp, kn, ks, m, _at(sink),
+            1.0 / math.sqrt(D) if scale is None else scale, _at(workspace), ws_bytes, out.data_ptr(), _DT[out.dtype],
+            _raw_stream(dev)), what)
     return out
 
 

@@ -11,9 +11,10 @@
 // All three move each row once and compute little, so memory bounds them: the
 // large calls by HBM, the decode calls by latency.  A lane owns both elements of
 // every pair that it rotates (see Unit), so a row needs no exchange but the sum
-// of the norm.  The angles of a token are shared by all its rows: a CTA builds
-// cos / sin once per token in shared memory while its first rows' loads are in
-// flight.
+// of the norm.  Every warp is on its own: its task is a range of rows of one
+// token, or the rows of a few tokens that have few; it issues the first rows'
+// loads, then looks its tokens up and computes their angles once, shared by all
+// the task's rows through its own part of shared memory.
 #include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -35,9 +36,8 @@ uint32_t read_clear_err_rows() {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTokens = kWarps;        // tokens per CTA: a warp looks up each
+constexpr int kMaxTokens = 8;             // tokens of a task
+constexpr int kMaxWarps = 8;
 
 struct RowSetDesc {                       // rows x[i, h, :] of one tensor
   const void* x;
@@ -45,6 +45,9 @@ struct RowSetDesc {                       // rows x[i, h, :] of one tensor
   const float* gain;                      // [D] or null
   int64_t x_tok, x_head, y_tok, y_head;   // strides in elements
   int H;
+  // tasks: tokens each; rows of each token; tasks that a group of tokens takes
+  int tpt, rpt, chunks;
+  int64_t tasks;
 };
 
 struct RowsParams {
@@ -55,9 +58,9 @@ struct RowsParams {
   int64_t n_tok;
   const double* inv_freq;                 // [r / 2]
   int D, r, r0, interleaved, norm;
-  float sign, mscale, eps;                // sign -1: the inverse rotation
+  float sign, mscale, eps, inv_d;         // sign -1: the inverse rotation; inv_d = 1 / D
   int units, lpr;                         // units of a row, lanes per row (a power of two)
-  int tpb, rows, rchunk;                  // tokens per CTA; rows per token; rows per CTA of each token
+  int cs_per_warp;                        // shared-memory angles of a warp
   // paged destination
   PageTable pt;
   uint8_t* nope;                          // e4m3 pages
@@ -67,27 +70,44 @@ struct RowsParams {
 
 enum Dest { DENSE = 0, PAGED = 1, PAGED_E4M3 = 2 };
 
-// 8 consecutive elements
-__device__ __forceinline__ void unpack8(const uint4 (&raw)[1], float* v) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) { const float2 f = __bfloat1622float2(h[i]); v[2 * i] = f.x; v[2 * i + 1] = f.y; }
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
 }
-__device__ __forceinline__ void unpack8(const uint4 (&raw)[2], float* v) {
-  const float* f = reinterpret_cast<const float*>(raw);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = f[i];
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return r;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+
+// 8 consecutive elements as 4 pairs
+__device__ __forceinline__ void unpack8(const uint4 (&raw)[1], float2* v) {
+  const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack8(const uint4 (&raw)[2], float2* v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[2 * i] = make_float2(__uint_as_float(raw[i].x), __uint_as_float(raw[i].y));
+    v[2 * i + 1] = make_float2(__uint_as_float(raw[i].z), __uint_as_float(raw[i].w));
+  }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float2* v) {
   uint4 a;
   __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&a);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(v[i]);
   *reinterpret_cast<uint4*>(p) = a;
 }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8(float* p, const float2* v) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
 
 // A unit is two chunks of 8 elements.  The r / 16 rotated units come first:
@@ -121,22 +141,44 @@ __device__ __forceinline__ Unit unit_of(const RowsParams& p, int u) {
   return w;
 }
 
-// UPL: units per lane; K: rows in flight per lane group.
+// Sequence of token i by one thread, -1 if it has none.
+__device__ __forceinline__ int find_seq(const int32_t* cu_q, int n_seq, int64_t i) {
+  if (i < cu_q[0] || i >= cu_q[n_seq]) return -1;
+  int lo = 0, hi = n_seq;                 // the last b with cu_q[b] <= i
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu_q[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// UPL: units per lane; K: row groups (32 / lpr rows) in flight per warp.
+// Two groups and 24 warps an SM (80 registers) were the best of the measured
+// splits: 4,850 tokens of 64 + 1 rows of 512 bf16 take 122 us (5.4 TB/s, 0.82 of
+// the copy rate) against 168 us with 32 warps (64 registers, spills) and 162 us
+// with four groups and 16 warps; 11,700 tokens of 64 rows of 128, turned whole,
+// 76 us (5.35 TB/s).  The issue slots, not DRAM, were full before the float32
+// pairs (mul2, fma2) and the shared look-ups: 390 instructions a row, 142 us.
 template <typename Tin, typename Tout, int UPL, int K, int DEST>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(32 * kMaxWarps, UPL == 4 ? 1 : sizeof(Tin) * UPL > 2 ? 2 : 3)
 rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int NV = sizeof(Tin) / 2;     // 16-byte vectors per chunk
-  extern __shared__ float2 s_cs[];        // [tpb][r / 2]
-  __shared__ int64_t s_pos[kMaxTokens];   // position, or -1: the token's rows are left alone
-  __shared__ int s_seq[kMaxTokens];
+  extern __shared__ float2 s_angles[];    // [warps][cs_per_warp]
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t tok0 = (int64_t)blockIdx.x * p.tpb;
-  const int row0 = blockIdx.y * p.rchunk;
-  const int nr = min(p.rchunk, p.rows - row0);
-  const int total = p.tpb * nr;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t task = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+  const int si = task >= p.set[0].tasks;
+  const RowSetDesc& st = p.set[si];
+  if (si) task -= p.set[0].tasks;
+  if (task >= st.tasks) return;           // warps do not wait for one another
+  const int64_t tok0 = task / st.chunks * st.tpt;
+  const int h0 = (int)(task % st.chunks) * st.rpt;
+  const int nr = min(st.rpt, st.H - h0);
+  const int nt = (int)min((int64_t)st.tpt, p.n_tok - tok0);
+  const int total = nt * nr;
   const int gpw = 32 / p.lpr, gl = lane / p.lpr, ul = lane % p.lpr;
+  const Tin* x0 = static_cast<const Tin*>(st.x) + tok0 * st.x_tok + h0 * st.x_head;
 
   Unit un[UPL];
   bool uv[UPL];
@@ -147,143 +189,153 @@ rows_kernel(const __grid_constant__ RowsParams p) {
     un[i] = unit_of(p, uv[i] ? u : 0);
   }
 
+  // Row lr of the task: token tok0 + lr / nr, head h0 + lr % nr.  K row groups
+  // are in flight: a group's registers are refilled as soon as it is unpacked.
+  // lr / nr by a product: lr < 1024 and nr <= 128 where a task has several tokens
+  const uint32_t rcp = nt == 1 ? 0 : (65535u + nr) / nr;
+  auto token_of = [&](int lr) { return (int)(((uint32_t)lr * rcp) >> 16); };
   uint4 raw[K][UPL][2][NV];
-  // Row `lr` of this CTA: token lr / nr, row row0 + lr % nr of its rows.
-  auto load_rows = [&](int base) {
+  auto load_row = [&](int k, int lr) {
+    if (lr >= total) return;
+    const int tl = token_of(lr);
+    const Tin* src = x0 + tl * st.x_tok + (lr - tl * nr) * st.x_head;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int lr = base + k * kWarps * gpw;
-      const int tl = lr / nr;
-      if (lr >= total || tok0 + tl >= p.n_tok) continue;
-      const int rr = row0 + lr % nr;
-      const RowSetDesc& st = p.set[rr >= p.set[0].H];
-      const int h = rr >= p.set[0].H ? rr - p.set[0].H : rr;
-      const Tin* src = static_cast<const Tin*>(st.x) + (tok0 + tl) * st.x_tok + h * st.x_head;
+    for (int i = 0; i < UPL; ++i)
+      if (uv[i])
 #pragma unroll
-      for (int i = 0; i < UPL; ++i)
-        if (uv[i])
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int n = 0; n < NV; ++n) raw[k][i][c][n] = reinterpret_cast<const uint4*>(src + un[i].d[c])[n];
-    }
+          for (int n = 0; n < NV; ++n) raw[k][i][c][n] = reinterpret_cast<const uint4*>(src + un[i].d[c])[n];
   };
-  const int first = warp * gpw + gl;
-  load_rows(first);
+#pragma unroll
+  for (int k = 0; k < K; ++k) load_row(k, gl + k * gpw);
 
-  // positions: a warp looks up each token of the CTA
-  if (warp < p.tpb) {
-    const int64_t i = tok0 + warp;
-    int b = -1;
-    if (i < p.n_tok) b = find_seq_warp(p.cu_q, p.n_seq, i, lane);
-    if (lane == 0) {
-      s_seq[warp] = b;
-      s_pos[warp] = b < 0 ? -1 : p.q_pos[b] + (i - p.cu_q[b]);
+  // the gains of a lane's only unit stay in registers
+  auto load_gain = [&](int d) {
+    return __ldg(reinterpret_cast<const float4*>(st.gain + d));
+  };
+  float4 gain[4];
+  if (UPL == 1 && st.gain)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) gain[c] = load_gain(un[0].d[c >> 1] + 4 * (c & 1));
+
+  // lane l < nt: sequence and position of token tok0 + l; position -1: its rows are left alone
+  int seq = -1;
+  int64_t pos = -1, slot = -1;            // slot: its row of the page store
+  if (lane < nt) {
+    seq = find_seq(p.cu_q, p.n_seq, tok0 + lane);
+    if (seq >= 0) pos = p.q_pos[seq] + (tok0 + lane - p.cu_q[seq]);
+    if (DEST != DENSE && pos >= 0) {
+      slot = page_row(p.pt, seq, pos);
+      if (slot < 0) atomicOr(&g_err_rows, DEV_ERR_BAD_INDEX);
     }
   }
-  __syncthreads();
-  // Angles in double, reduced to [-pi, pi] there (positions reach 2^20 and
-  // more), then cos and sin in float of the reduced angle.
+  // Angles in double (positions reach 2^20 and more), as the part of a turn in
+  // [-1/2, 1/2], then cos and sin in float of that part times 2 pi.
+  float2* s_cs = s_angles + warp * p.cs_per_warp;
   const int half = p.r >> 1;
-  for (int e = tid; e < p.tpb * half; e += kThreads) {
-    const int64_t pos = s_pos[e / half];
-    if (pos < 0) continue;
-    double a = (double)pos * p.inv_freq[e % half];
-    a -= rint(a * 0.15915494309189533577) * 6.283185307179586477;
-    float sn, cs;
-    sincosf((float)a, &sn, &cs);
-    s_cs[e] = make_float2(cs * p.mscale, sn * p.mscale * p.sign);
+  for (int e0 = 0; e0 < nt * half; e0 += 32) {
+    const int e = e0 + lane;
+    const int tl = e / half;
+    const int64_t ps = __shfl_sync(0xffffffffu, pos, tl & 31);
+    if (e < nt * half) {
+      const double turns = (double)ps * p.inv_freq[e - tl * half] * 0.15915494309189533577;
+      float sn, cs;
+      sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cs);
+      s_cs[e] = make_float2(cs * p.mscale, sn * p.mscale * p.sign);
+    }
   }
-  __syncthreads();
+  __syncwarp();
 
-  for (int base = first; base - first < total; base += K * kWarps * gpw) {     // uniform over the CTA
-    if (base != first) load_rows(base);
+  for (int base = gl; base - gl < total; base += K * gpw) {     // uniform over the warp
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int lr = base + k * kWarps * gpw;
-      const int tl = min(lr / nr, p.tpb - 1);
-      const int rr = row0 + lr % nr;
-      const int64_t pos = s_pos[tl];
-      const bool on = lr < total && pos >= 0;
-      const int si = rr >= p.set[0].H ? 1 : 0;
-      const RowSetDesc& st = p.set[si];
-      const int h = rr - (si ? p.set[0].H : 0);
-      float v[UPL][16];
+      if (base - gl + k * gpw >= total) break;                  // uniform too
+      const int lr = base + k * gpw;
+      const int tl = token_of(lr) & 31;
+      const int64_t ps = __shfl_sync(0xffffffffu, pos, tl);
+      const bool on = lr < total && ps >= 0;
+      float2 v[UPL][8];
 #pragma unroll
       for (int i = 0; i < UPL; ++i) {
-        if (on && uv[i]) {
+        if (uv[i]) {
           unpack8(raw[k][i][0], v[i]);
-          unpack8(raw[k][i][1], v[i] + 8);
+          unpack8(raw[k][i][1], v[i] + 4);
         } else {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) v[i][c] = 0.f;
+          for (int c = 0; c < 8; ++c) v[i][c] = make_float2(0.f, 0.f);
         }
       }
+      load_row(k, lr + K * gpw);
       if (p.norm) {
-        float ss = 0.f;
+        float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < UPL; ++i)
 #pragma unroll
-          for (int c = 0; c < 16; ++c) ss = fmaf(v[i][c], v[i][c], ss);
-        for (int o = p.lpr >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(ss / (float)p.D + p.eps);
+          for (int c = 0; c < 8; ++c) s2 = fma2(v[i][c], v[i][c], s2);
+        float ss = s2.x + s2.y;
 #pragma unroll
-        for (int i = 0; i < UPL; ++i) {
+        for (int o = 16; o > 0; o >>= 1) {
+          const float t = __shfl_xor_sync(0xffffffffu, ss, o);
+          if (o < p.lpr) ss += t;
+        }
+        const float inv = rsqrtf(fmaf(ss, p.inv_d, p.eps));
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float4* g4 = reinterpret_cast<const float4*>(st.gain + un[i].d[c]);
+        for (int i = 0; i < UPL; ++i)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float4 g = st.gain ? __ldg(g4 + q) : make_float4(1.f, 1.f, 1.f, 1.f);
-              float* w = v[i] + 8 * c + 4 * q;
-              w[0] *= inv * g.x; w[1] *= inv * g.y; w[2] *= inv * g.z; w[3] *= inv * g.w;
+          for (int c = 0; c < 8; ++c) v[i][c] = mul2(v[i][c], make_float2(inv, inv));
+        if (st.gain) {
+#pragma unroll
+          for (int i = 0; i < UPL; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float4 g = UPL == 1 ? gain[c] : load_gain(un[i].d[c >> 1] + 4 * (c & 1));
+              v[i][2 * c] = mul2(v[i][2 * c], make_float2(g.x, g.y));
+              v[i][2 * c + 1] = mul2(v[i][2 * c + 1], make_float2(g.z, g.w));
             }
-          }
         }
       }
 #pragma unroll
       for (int i = 0; i < UPL; ++i) {
         if (!(on && un[i].rot)) continue;
-        const float2* cs = s_cs + tl * half;
+        // (cos, sin) of two pairs at a time
+        const float4* cs = reinterpret_cast<const float4*>(s_cs + tl * half);
         if (p.interleaved) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 w = cs[un[i].j[c] + j];
-              const float a = v[i][8 * c + 2 * j], b = v[i][8 * c + 2 * j + 1];
-              v[i][8 * c + 2 * j] = a * w.x - b * w.y;
-              v[i][8 * c + 2 * j + 1] = a * w.y + b * w.x;
-            }
+          for (int c = 0; c < 4; ++c) {
+            const float4 w = cs[(un[i].j[c >> 1] >> 1) + (c & 1)];
+            float2& e = v[i][2 * c];
+            float2& f = v[i][2 * c + 1];
+            e = make_float2(e.x * w.x - e.y * w.y, e.x * w.y + e.y * w.x);
+            f = make_float2(f.x * w.z - f.y * w.w, f.x * w.w + f.y * w.z);
+          }
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 w = cs[un[i].j[0] + j];
-            const float a = v[i][j], b = v[i][8 + j];
-            v[i][j] = a * w.x - b * w.y;
-            v[i][8 + j] = a * w.y + b * w.x;
+          for (int j = 0; j < 4; ++j) {
+            const float4 w = cs[(un[i].j[0] >> 1) + j];
+            const float2 c2 = make_float2(w.x, w.z), s2 = make_float2(w.y, w.w);
+            const float2 a = v[i][j], b = v[i][4 + j];
+            v[i][j] = fma2(a, c2, mul2(b, make_float2(-s2.x, -s2.y)));
+            v[i][4 + j] = fma2(b, c2, mul2(a, s2));
           }
         }
       }
       if constexpr (DEST == DENSE) {
         if (on) {
-          Tout* dst = static_cast<Tout*>(st.y) + (tok0 + tl) * st.y_tok + h * st.y_head;
+          Tout* dst = static_cast<Tout*>(st.y) + (tok0 + tl) * st.y_tok + (h0 + lr - tl * nr) * st.y_head;
 #pragma unroll
           for (int i = 0; i < UPL; ++i)
-            if (uv[i]) { store8(dst + un[i].d[0], v[i]); store8(dst + un[i].d[1], v[i] + 8); }
+            if (uv[i]) { store8(dst + un[i].d[0], v[i]); store8(dst + un[i].d[1], v[i] + 4); }
         }
       } else {
-        int64_t row = -1;
-        if (on) {
-          row = page_row(p.pt, s_seq[tl], pos);
-          if (row < 0 && ul == 0) atomicOr(&g_err_rows, DEV_ERR_BAD_INDEX);
-        }
+        const int64_t at = __shfl_sync(0xffffffffu, slot, tl);
+        const int64_t row = on ? at : -1;
         if constexpr (DEST == PAGED) {
           if (row >= 0) {
             Tout* dst = static_cast<Tout*>(st.y) + row * p.D;
 #pragma unroll
             for (int i = 0; i < UPL; ++i)
-              if (uv[i]) { store8(dst + un[i].d[0], v[i]); store8(dst + un[i].d[1], v[i] + 8); }
+              if (uv[i]) { store8(dst + un[i].d[0], v[i]); store8(dst + un[i].d[1], v[i] + 4); }
           }
         } else {
           // s = max|.| / 448 over the D - r dims outside the rotated part
@@ -292,10 +344,25 @@ rows_kernel(const __grid_constant__ RowsParams p) {
           for (int i = 0; i < UPL; ++i)
             if (uv[i] && !un[i].rot)
 #pragma unroll
-              for (int c = 0; c < 16; ++c) am = fmaxf(am, fabsf(v[i][c]));
-          for (int o = p.lpr >> 1; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+              for (int c = 0; c < 8; ++c) am = fmaxf(am, fmaxf(fabsf(v[i][c].x), fabsf(v[i][c].y)));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const float t = __shfl_xor_sync(0xffffffffu, am, o);
+            if (o < p.lpr) am = fmaxf(am, t);
+          }
           float s = am / 448.f;
           if (s == 0.f) s = 1.f;
+          // one division a row, not one an element; rows so small that the
+          // inverse would overflow are scaled up first
+          float rs = 1.f / s;
+          if (s < 1e-37f) {
+            rs = 1.f / (s * 0x1p60f);
+#pragma unroll
+            for (int i = 0; i < UPL; ++i)
+              if (!un[i].rot)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[i][c] = mul2(v[i][c], make_float2(0x1p60f, 0x1p60f));
+          }
           if (row >= 0) {
             if (ul == 0) p.scale[row] = s;
 #pragma unroll
@@ -303,16 +370,16 @@ rows_kernel(const __grid_constant__ RowsParams p) {
               if (!uv[i]) continue;
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const float* w = v[i] + 8 * c;
                 if (un[i].rot) {
-                  store8(p.rope + row * p.r + (un[i].d[c] - p.r0), w);
+                  store8(p.rope + row * p.r + (un[i].d[c] - p.r0), v[i] + 4 * c);
                 } else {
                   uint32_t q[2];
 #pragma unroll
                   for (int n = 0; n < 2; ++n) {
-                    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(w[4 * n] / s, w[4 * n + 1] / s), __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(w[4 * n + 2] / s, w[4 * n + 3] / s), __NV_SATFINITE, __NV_E4M3);
-                    q[n] = a | (b << 16);
+                    const float2 r2 = make_float2(rs, rs);
+                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(v[i][4 * c + 2 * n], r2), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(v[i][4 * c + 2 * n + 1], r2), __NV_SATFINITE, __NV_E4M3);
+                    q[n] = lo | (hi << 16);
                   }
                   *reinterpret_cast<uint2*>(p.nope + row * (p.D - p.r) + un[i].d[c]) = make_uint2(q[0], q[1]);
                 }
@@ -327,24 +394,50 @@ rows_kernel(const __grid_constant__ RowsParams p) {
 
 template <typename Tin, typename Tout, int DEST>
 csa_status_t launch_rows(RowsParams& p, const char* fn, cudaStream_t st) {
-  p.rows = p.set[0].H + p.set[1].H;
-  if (p.n_tok == 0 || p.rows == 0 || p.units == 0) return CSA_OK;
+  if (p.n_tok == 0 || p.set[0].H + p.set[1].H == 0 || p.units == 0) return CSA_OK;
   p.lpr = 1;
   while (p.lpr < 32 && p.lpr < p.units) p.lpr *= 2;
-  // about 32 rows a CTA: whole tokens if they have fewer rows, else an even part of one token's rows
-  const int chunks = (p.rows + 32) / 33;
-  p.rchunk = (p.rows + chunks - 1) / chunks;
-  p.tpb = std::max(1, std::min(kMaxTokens, 32 / p.rows));
-  if (p.r > 0) p.tpb = std::min(p.tpb, 8192 / p.r);      // angles within 32 KB (r is at most 2048)
-  const int64_t gx = (p.n_tok + p.tpb - 1) / p.tpb;
-  if (gx > 0x7fffffff || chunks > 65535) return fail(CSA_ERR_UNSUPPORTED, "%s: too many rows", fn);
-  const dim3 grid((unsigned)gx, (unsigned)chunks);
-  const size_t smem = (size_t)p.tpb * (p.r / 2) * sizeof(float2);
   const int upl = (p.units + p.lpr - 1) / p.lpr;
+  const int per_pass = 32 / p.lpr * (upl == 1 ? 2 : 1);   // rows in flight of a warp
+  const int warps_wanted = num_sms() * 16;
+  p.inv_d = 1.f / (float)p.D;
+  p.cs_per_warp = 0;
+  int64_t tasks = 0;
+  for (RowSetDesc& s : p.set) {
+    s.tasks = 0;
+    s.tpt = s.rpt = s.chunks = 1;
+    if (s.H == 0) continue;
+    // A task has up to eight passes of rows, which share their token's look-up and
+    // angles; fewer where that leaves warps idle, so that a small batch is over
+    // sooner.
+    int want = 8 * per_pass;
+    while (want > per_pass && p.n_tok * s.H / want < warps_wanted) want /= 2;
+    if (want < per_pass) want = per_pass;
+    if (s.H >= want) {
+      s.chunks = (s.H + want - 1) / want;
+      s.rpt = (s.H + s.chunks - 1) / s.chunks;
+      s.chunks = (s.H + s.rpt - 1) / s.rpt;
+    } else {
+      s.rpt = s.H;
+      s.tpt = std::max(1, std::min(kMaxTokens, want / s.H));
+      while (s.tpt > 1 && (s.tpt * p.r > 1024 || p.n_tok * s.H / (s.tpt * s.H) < warps_wanted / 2)) --s.tpt;
+    }
+    s.tasks = (p.n_tok + s.tpt - 1) / s.tpt * s.chunks;
+    tasks += s.tasks;
+    p.cs_per_warp = std::max(p.cs_per_warp, s.tpt * (p.r / 2));
+  }
+  int warps = kMaxWarps;
+  while (warps > 1 && warps * p.cs_per_warp * sizeof(float2) > 32768) warps /= 2;
+  // a small batch spreads over all SMs
+  while (warps > 1 && tasks / warps < num_sms()) warps /= 2;
+  const int64_t gx = (tasks + warps - 1) / warps;
+  if (gx > 0x7fffffff) return fail(CSA_ERR_UNSUPPORTED, "%s: too many rows", fn);
+  const dim3 grid((unsigned)gx), block(32 * warps);
+  const size_t smem = (size_t)warps * p.cs_per_warp * sizeof(float2);
   cudaError_t e;
-  if (upl == 1) e = launch_pdl(rows_kernel<Tin, Tout, 1, 4, DEST>, grid, dim3(kThreads), smem, st, p);
-  else if (upl == 2) e = launch_pdl(rows_kernel<Tin, Tout, 2, 2, DEST>, grid, dim3(kThreads), smem, st, p);
-  else e = launch_pdl(rows_kernel<Tin, Tout, 4, 1, DEST>, grid, dim3(kThreads), smem, st, p);
+  if (upl == 1) e = launch_pdl(rows_kernel<Tin, Tout, 1, 2, DEST>, grid, block, smem, st, p);
+  else if (upl == 2) e = launch_pdl(rows_kernel<Tin, Tout, 2, 1, DEST>, grid, block, smem, st, p);
+  else e = launch_pdl(rows_kernel<Tin, Tout, 4, 1, DEST>, grid, block, smem, st, p);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return check_launch(fn);
 }

@@ -473,7 +473,7 @@ def test_binding_refusals(csa):
         (lambda: csa.csa_rope(x[:, 1:], c.cu, c.qp, w, out=x[:, :-1]), "overlap"), (lambda: csa.csa_rope(x, c.cu, c.qp, w, out=x[:1]), "shape"),
         (lambda: csa.csa_rope(x, c.cu, c.qp, w, out=x[:, :1].expand_as(x)), "overlap"),
         (lambda: csa.csa_qk_norm_rope(x, x[..., :64], c.cu, c.qp, w), "one dtype"), (lambda: csa.csa_qk_norm_rope(x, None, c.cu, c.qp, w, q_gain=torch.ones(64, device="cuda")), "q_gain"),
-        (lambda: csa.csa_qk_norm_rope(x, x, c.cu, c.qp, w, q_out=x, k_out=x), "overlap"),
+        (lambda: csa.csa_qk_norm_rope(x, x.clone(), c.cu, c.qp, w, q_out=x, k_out=x), "overlap"),
         (lambda: csa.csa_paged_append(x[:, 0], c.cu, c.qp, c.kw["tok_table"], c.kw["tok_pages"][..., :64].contiguous(), w), "pages"),
         (lambda: csa.csa_paged_append(x[:, 0], c.cu, c.qp, c.kw["tok_table"].long(), c.kw["tok_pages"], w), "block_table"),
         (lambda: csa.csa_paged_append(x[:, 0], c.cu, c.qp, c.kw["tok_table"], torch.zeros(4, 48, 128, device="cuda"), w), "power of two"),

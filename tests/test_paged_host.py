@@ -178,11 +178,12 @@ def test_binding_knows_overlapping_rows():
     assert csa._shares(base, base.bfloat16().view(torch.bfloat16)) is False
     assert csa._shares(base, base.view(torch.bfloat16)) and csa._shares(base[..., :64], base[..., 32:96])
     assert not csa._shares(base, torch.zeros(4, 3, 128))
+    assert csa._overlap(base, base) and not csa._overlap(base[0], base[1])
     with pytest.raises(csa.CsaError, match="overlap"):
-        csa._heads("f", "out", torch.zeros(1, 1, 128).expand(4, 3, 128), out=True)
+        csa._out_heads("f", "out", torch.zeros(1, 1, 128).expand(4, 3, 128))
     with pytest.raises(csa.CsaError, match="overlap"):
-        csa._heads("f", "out", torch.zeros(4 * 128).as_strided((3, 128), (64, 1)), out=True)
-    csa._heads("f", "out", base.transpose(0, 1), out=True)
+        csa._out_heads("f", "out", torch.zeros(4 * 128).as_strided((3, 128), (64, 1)))
+    assert csa._out_heads("f", "out", base.transpose(0, 1)) == (3, 4, 128, 128, 384)
 
 
 def test_oracle_attention_of_no_rows_is_zero():
