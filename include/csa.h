@@ -485,8 +485,9 @@ csa_status_t csa_paged_append(const void* rows, csa_dtype_t in_dtype, int64_t ro
  *   out [n_tok, H, D] F32 or BF16: bf16 tensor-core products (probabilities
  *     rounded to bf16), fp32 accumulation and softmax statistics.
  * Rows that a token does not see never reach its output, whatever they hold.
- * A visible row without a page is recorded as CSA_ERR_DEVICE and read as zeros;
- * rows behind max_pages * page_size are not visible.
+ * A visible row without a page is recorded as CSA_ERR_DEVICE, and the results of
+ * the tokens that see it mean nothing; rows behind max_pages * page_size are not
+ * visible.  A visible row with a NaN or an infinity puts NaN into the result.
  * workspace: csa_paged_attention_workspace(n_tok, n_seq, H, D) bytes (0 from
  * about 75 tokens on), 16-byte aligned; calls sharing one must be ordered on
  * one stream, and a captured graph keeps its own. */

@@ -71,7 +71,7 @@ extern "C" csa_status_t csa_check_device_error(cudaStream_t stream) {
   if (e != cudaSuccess)
     return csa::fail(CSA_ERR_CUDA, "csa_check_device_error: stream sync failed: %s", cudaGetErrorString(e));
   uint32_t w = csa::read_clear_err_indexer() | csa::read_clear_err_attention() | csa::read_clear_err_proj() |
-               csa::read_clear_err_compress() | csa::read_clear_err_rows() | csa::read_clear_err_selftest();
+               csa::read_clear_err_compress() | csa::read_clear_err_rows() | csa::read_clear_err_pair() | csa::read_clear_err_selftest();
   if (w & 1u) return csa::fail(CSA_ERR_TIMEOUT, "a bounded on-chip wait expired (device error word 0x%x)", w);
   if (w) return csa::fail(CSA_ERR_DEVICE, "a kernel recorded an out-of-range gather index or a missing page (device error word 0x%x)", w);
   return CSA_OK;

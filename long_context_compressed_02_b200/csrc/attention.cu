@@ -52,6 +52,7 @@
 #include "tc.cuh"
 #include "tmap.cuh"
 #include "batch.cuh"
+#include "paged.cuh"
 
 namespace csa {
 
@@ -67,6 +68,11 @@ uint32_t read_clear_err_attention() {
 namespace {
 
 constexpr int kThreads = 352;      // 11 warps: 4 softmax + epilogue, 4 loaders, 3 MMA issuers
+// Paged e4m3 calls have a second group of 4 loader warps (11 - 14): the groups
+// take alternate half chunks, so one group's loads are in flight while the other
+// converts.
+template <int KV, bool PAGED>
+constexpr int attn_threads() { return PAGED && KV == 2 /* e4m3 */ ? kThreads + 128 : kThreads; }
 constexpr int kNQ = 64;            // query rows (heads) per tile = MMA N
 constexpr int kRows = 64;          // KV rows per ring slot (a half chunk) = M of the S MMA
 constexpr float kTau = 8.0f;       // lazy-rescale threshold (log2 units)
@@ -244,8 +250,8 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, SplitPlan& s, int
   __syncthreads();
 }
 
-// Item -> sequence, token of the sequence, range, row of the batch.  A paged
-// call's item may be a padding row, which belongs to no sequence (false).
+// Item -> sequence, token of the sequence, range, row of the batch.  False for
+// the rows of a paged call that are left alone: padding, negative positions.
 struct Item { int b, t, sp; int64_t bt; int per; };
 template <bool PAGED>
 __device__ __forceinline__ bool locate_warp(const AttnParams& p, const SplitPlan* plan, int64_t item, int lane, Item& it) {
@@ -261,12 +267,13 @@ __device__ __forceinline__ bool locate_warp(const AttnParams& p, const SplitPlan
       it.sp = (int)(item - f0) % ns;
       it.bt = c0 + it.t;
       it.per = plan->per;
-      return it.bt >= 0 && it.bt < p.n_tok;
+      return it.bt >= 0 && it.bt < p.n_tok && p.q_pos[it.b] + it.t >= 0;
     }
     it.bt = item;
     it.b = find_seq_warp(p.cu_q, p.n_seq, item, lane);
     if (it.b < 0) return false;
     it.t = (int)(item - p.cu_q[it.b]);
+    return p.q_pos[it.b] + it.t >= 0;
   } else {
     it.bt = item / p.n_split;
     it.sp = (int)(item % p.n_split);
@@ -334,6 +341,43 @@ __device__ __forceinline__ void e4m3x16_to_float(uint4 raw, float scale, float* 
   }
 }
 
+// e4m3 x 16 -> 16 bf16, exactly: sign and the 7 low bits (exponent, mantissa) go
+// to their places in a bf16, whose exponent is then 120 short; the product with
+// 2^120 restores it, for subnormal codes too.  NaN codes come out as numbers
+// and leave bit 7 of a byte of `nan` set.
+__device__ __forceinline__ void codes_to_bf16(uint4 raw, uint4& lo, uint4& hi, uint32_t& nan) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t x = __byte_perm(w[i], 0, j ? 0x3424 : 0x1404);      // bytes to the high halves
+      const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+      const uint32_t k = 0x7b807b80u;                                    // 2^120 twice
+      const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&k));
+      o[2 * i + j] = *reinterpret_cast<const uint32_t*>(&z);
+    }
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+__device__ __forceinline__ bool has_nan_code(uint4 r) {
+  const uint32_t n = ((r.x & 0x7f7f7f7fu) + 0x01010101u) | ((r.y & 0x7f7f7f7fu) + 0x01010101u) |
+                     ((r.z & 0x7f7f7f7fu) + 0x01010101u) | ((r.w & 0x7f7f7f7fu) + 0x01010101u);
+  return (n & 0x80808080u) != 0;
+}
+// 8 bf16 times f
+__device__ __forceinline__ void bf16x8_scaled(uint4 raw, float f, float* v) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16) * f;
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * f;
+  }
+}
+
 // 64 fp32 values (one 128-byte slab of a row, after conversion) -> row r of a
 // 128-byte-swizzled bf16 slab.
 __device__ __forceinline__ void store_row_slab_f32(uint8_t* slab_base, int r, const float* v) {
@@ -381,7 +425,7 @@ __device__ __forceinline__ float2 col_reduce16(float (&v)[16], int lane) {
 }
 
 template <int D, int KV, int EPI, bool PAGED = false>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(attn_threads<KV, PAGED>(), 1)
 attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_q,
             const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_tok) {
   constexpr int NS = D / 64;                 // 128-byte slabs per row
@@ -422,6 +466,8 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
   int64_t* s_items = reinterpret_cast<int64_t*>(item_empty + 4);   // [4]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_items + 4);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+  constexpr bool kCodes = PAGED && KV == KV_FP8;     // slots hold e4m3 codes, row scales apart
+  __shared__ float s_scale[kCodes ? 2 : 1][kRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // inverse RoPE frequencies, once per CTA: inv_freq_j = base^(-2j / rope_dim)
@@ -448,9 +494,9 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
   SplitPlan* plan = nullptr;
   if (PAGED && p.max_items > 0) {
     plan = reinterpret_cast<SplitPlan*>(s_abort + 1);
-    make_plan(p, *plan, tid, kThreads);
+    make_plan(p, *plan, tid, blockDim.x);
     if (blockIdx.x == 0)
-      for (int b = tid; b <= p.n_seq; b += kThreads) p.plan[b] = plan->first[b];
+      for (int b = tid; b <= p.n_seq; b += blockDim.x) p.plan[b] = plan->first[b];
   }
   const int64_t n_items = !PAGED ? (int64_t)p.n_seq * p.T * p.n_split
                                  : plan ? min(plan->first[p.n_seq], p.max_items) : p.n_tok;
@@ -473,9 +519,10 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     return it;
   };
 
-  if (warp >= 4 && warp < 8) {
+  if ((warp >= 4 && warp < 8) || warp >= 11) {
     // ============================ loaders
-    const int lt = tid - 128;                 // 0..127
+    const int grp = warp >= 11 ? 1 : 0;
+    const int lt = grp ? tid - 352 : tid - 128;   // 0..127 of the group
     const int lw = lt >> 5;                   // loader warp: rows 16 lw .. 16 lw + 15 of a slot (gathers)
     const int my_r = lt & 63, part = lt >> 6; // converting loads: one row, slabs part, part + 2, ...
     uint32_t g = 0, qcount = 0;
@@ -490,9 +537,11 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per);
       if (rs.c1 <= rs.c0) continue;
       // ---- Q tile: 64 rows x NS slabs of 128 B
-      if (!wait_bar(q_free, (qcount & 1) ^ 1, abort_flag)) { ok = false; break; }
+      if (grp == 0 && !wait_bar(q_free, (qcount & 1) ^ 1, abort_flag)) { ok = false; break; }
       ++qcount;
-      if (p.tma_q) {
+      if (grp != 0) {
+        // the first group's
+      } else if (p.tma_q) {
         // 64 query rows (the token's heads; rows past H belong to the next token or
         // are zero-filled, and their columns are never written out)
         if (lt == 0) {
@@ -535,8 +584,38 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       }
       // ---- KV half chunks into the two-slot ring
       int pre_c = -1;                    // half chunk whose gathered row index pre_row holds
-      typename std::conditional<PAGED, int64_t, int32_t>::type pre_row = 0;
+      int32_t pre_row = 0;
+      // Paged rows: bulk prefetch of a half chunk into L2, page by page.  The ring
+      // holds two half chunks, too few to cover the latency of HBM; kAhead half
+      // chunks ahead the loads find their rows in L2.
+      constexpr int kAhead = kCodes ? 4 : 3;
+      auto prefetch = [&](int cc) {
+        if (cc >= rs.c1) return;
+        const bool w = cc < rs.nh2;
+        const PageTable& pt = w ? p.pt2 : p.pt1;
+        const int64_t at = (int64_t)(w ? cc : cc - rs.nh2) * kRows;
+        const int64_t r0 = (w ? rs.lo2 : 0) + at, r1 = r0 + min((int64_t)kRows, (w ? rs.n2 : rs.n1) - at);
+        const int64_t pg1 = (r1 - 1) >> pt.ps_log2;
+        for (int64_t pg = (r0 >> pt.ps_log2) + lane; pg <= pg1; pg += 32) {
+          const int64_t a = max(r0, pg << pt.ps_log2), e = min(r1, (pg + 1) << pt.ps_log2);
+          const int64_t g0 = page_row(pt, b, a);
+          if (g0 < 0) continue;
+          const uint32_t n = (uint32_t)(e - a);
+          if (KV == KV_FP8 && !w) {
+            prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(p.kv) + g0 * (D - 64), n * (D - 64));
+            prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(p.kv_rope) + g0 * 128, n * 128);
+            if (pt.ps_log2 >= 2)         // whole 16-byte pieces lie within the page
+              prefetch_l2_bulk(p.kv_scale + (g0 & ~(int64_t)3), 4 * (uint32_t)(((g0 & 3) + n + 3) & ~3u));
+          } else {
+            prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(w ? p.kv2 : p.kv) + g0 * D * 2, n * (D * 2));
+          }
+        }
+      };
+      if (PAGED && grp == 0 && lw == 0)
+        for (int i = 1; i <= kAhead; ++i) prefetch(rs.c0 + i);
       for (int c = rs.c0; c < rs.c1 && ok; ++c, ++g) {
+        if (kCodes && (int)(g & 1) != grp) continue;
+        if (PAGED && lw == 0) prefetch(c + kAhead + 1);
         const int slot = g & 1;
         const uint32_t fpar = ((g >> 1) & 1) ^ 1;     // completion of PV(g - 2), which read this slot
         uint8_t* sl_base = sKV + slot * kSlot;
@@ -649,7 +728,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
             int64_t row1 = 0;
             if constexpr (PAGED) {
               if (vld) {
-                row1 = pre_c == cc ? pre_row : page_row(p.pt1, b, r1);
+                row1 = page_row(p.pt1, b, r1);
                 if (row1 < 0) { atomicOr(&g_err_attn, DEV_ERR_BAD_INDEX); vld = false; row1 = 0; }
               }
             } else if (vld) {
@@ -694,15 +773,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
             const int r0 = (c + 1 - rs.nh2) * kRows;
             const int nr = min(kRows, rs.n1 - r0);
             if constexpr (PAGED) {
-              // the next half chunk's rows, looked up ahead; each row's bytes into L2
-              if (16 * lw + rl < nr) {
-                pre_row = page_row(p.pt1, b, r0 + 16 * lw + rl);
-                pre_c = c + 1;
-                if (lane < 16 && pre_row >= 0) {
-                  prefetch_l2_bulk(kvn + (long long)pre_row * kNope, kNope);
-                  prefetch_l2_bulk(kvr + (long long)pre_row * 128, 128);
-                }
-              }
+              // prefetched above
             } else if (rs.idx == nullptr) {
               const long long g0 = (long long)b * p.cap + r0;
               if (lt == 0) prefetch_l2_bulk(kvn + g0 * kNope, (uint32_t)(nr * kNope));
@@ -712,6 +783,67 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
               pre_row = __ldg(rs.idx + r0 + 16 * lw + rl);
               pre_c = c + 1;
             }
+          }
+          if constexpr (kCodes) {
+            // The slot takes the codes themselves (exact in bf16) and the RoPE part
+            // divided by the row's scale; the softmax multiplies logits and
+            // probabilities by the scale, so the nope dims are rounded nowhere and a
+            // code costs 5 integer instructions for 2 instead of conversions through
+            // float32.  Scales below 2^-100 count as 2^-100: their rows' codes are
+            // worth nothing next to any RoPE part, which must not overflow.
+            sc = fabsf(sc) < 0x1p-100f ? 0x1p-100f : sc;
+            const float isc = 1.f / sc;
+            uint32_t nan = 0;
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt) {
+              if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
+              if (tt < NT - 1) {
+                uint8_t* dst = sl_base + (2 * tt + ((lane & 7) >> 2)) * kSlab;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int rr = 16 * lw + 4 * i + (lane >> 3);
+                  uint4 lo, hi;
+                  codes_to_bf16(raw[tt][i], lo, hi, nan);
+                  st_shared16(dst + swz128(rr, 2 * (lane & 3)), lo);
+                  st_shared16(dst + swz128(rr, 2 * (lane & 3) + 1), hi);
+                }
+              } else {
+                uint8_t* dst = sl_base + (2 * tt) * kSlab;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int rr = 16 * lw + 8 * i + (lane >> 2);
+                  uint4 lo, hi;
+                  codes_to_bf16(raw[tt][i], lo, hi, nan);
+                  st_shared16(dst + swz128(rr, 2 * (lane & 3)), lo);
+                  st_shared16(dst + swz128(rr, 2 * (lane & 3) + 1), hi);
+                }
+                uint8_t* dr = sl_base + (NS - 1) * kSlab;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float f = __shfl_sync(0xffffffffu, isc, 4 * i + (lane >> 3));
+                  float v[8];
+                  bf16x8_scaled(rope[i], f, v);
+                  st_shared16(dr + swz128(16 * lw + 4 * i + (lane >> 3), lane & 7), to_bf16x8(v));
+                }
+                // A NaN code has become a number: its row's scale carries it instead.
+                // Lane l's pieces belong to rows 4 i + l / 8 (all pairs but the last)
+                // and 8 i + l / 4, so a warp with a NaN looks each piece up again.
+                if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0)) {
+#pragma unroll
+                  for (int t2 = 0; t2 < NT; ++t2)
+#pragma unroll
+                    for (int i = 0; i < (t2 < NT - 1 ? 4 : 2); ++i) {
+                      const unsigned m = __ballot_sync(0xffffffffu, has_nan_code(raw[t2][i]));
+                      const int per = t2 < NT - 1 ? 8 : 4, rows = 32 / per;
+                      if (rl / rows == i && ((m >> ((rl % rows) * per)) & ((1u << per) - 1u))) sc = CUDART_NAN_F;
+                    }
+                }
+                if (lane < 16) s_scale[slot][16 * lw + rl] = sc;
+              }
+              fence_proxy_async_smem();
+              mbar_arrive(&full[tt]);
+            }
+            continue;
           }
           // row scales to the converting lanes (waits for the scale loads only now)
           float sc4[4], sc2[2];
@@ -928,6 +1060,18 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         const int h0 = (win ? c : c - rs.nh2) * kRows;
         const int nset = win ? rs.n2 : rs.n1;
         const bool vA = h0 + rA < nset, vB = h0 + rB < nset;
+        float scA = 1.f, scB = 1.f;
+        if (kCodes && !win) {
+          // the scales came with the slot's last slab pair (complete: S was made from it)
+          if (!wait_bar(&kv_full[sb * NT + NT - 1], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+          scA = s_scale[sb][rA];
+          scB = s_scale[sb][rB];
+#pragma unroll
+          for (int cc = 0; cc < 8; ++cc) {
+            x[4 * cc] *= scA; x[4 * cc + 1] *= scA;
+            x[4 * cc + 2] *= scB; x[4 * cc + 3] *= scB;
+          }
+        }
 #pragma unroll
         for (int cc = 0; cc < 8; ++cc) {                   // raw logits; scale folded below
           if (!vA) { x[4 * cc] = -CUDART_INF_F; x[4 * cc + 1] = -CUDART_INF_F; }
@@ -1002,8 +1146,13 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         const uint32_t pb = smem_u32(sP + sb * kPBuf) + 4 * (lane & 3);
 #pragma unroll
         for (int cc = 0; cc < 8; ++cc) {
-          st_shared4(pb + swz128(rA, cc), pack_bf16(pr[4 * cc], pr[4 * cc + 1]));
-          st_shared4(pb + swz128(rB, cc), pack_bf16(pr[4 * cc + 2], pr[4 * cc + 3]));
+          if constexpr (kCodes) {       // the row's scale goes into its probabilities
+            st_shared4(pb + swz128(rA, cc), pack_bf16(pr[4 * cc] * scA, pr[4 * cc + 1] * scA));
+            st_shared4(pb + swz128(rB, cc), pack_bf16(pr[4 * cc + 2] * scB, pr[4 * cc + 3] * scB));
+          } else {
+            st_shared4(pb + swz128(rA, cc), pack_bf16(pr[4 * cc], pr[4 * cc + 1]));
+            st_shared4(pb + swz128(rB, cc), pack_bf16(pr[4 * cc + 2], pr[4 * cc + 3]));
+          }
         }
 #pragma unroll
         for (int cc = 0; cc < 8; ++cc) {
@@ -1274,8 +1423,8 @@ attn_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, co
 // empty ranges, whose output was not written.
 __global__ void __launch_bounds__(128)
 paged_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, const int32_t* __restrict__ plan,
-                   const float* __restrict__ sink, const int32_t* __restrict__ cu_q, int n_seq, int max_items, int H,
-                   int D, void* __restrict__ out, int out_bf16) {
+                   const float* __restrict__ sink, const int32_t* __restrict__ cu_q, const int64_t* __restrict__ q_pos,
+                   int n_seq, int max_items, int H, int D, void* __restrict__ out, int out_bf16) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.y * 4 + (threadIdx.x >> 5);
@@ -1285,6 +1434,7 @@ paged_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, c
   const int b = find_seq_warp(cu_q, n_seq, bt, lane);
   if (b < 0 || h >= H) return;
   const int c0 = cu_q[b], f0 = plan[b];
+  if (q_pos[b] + (bt - c0) < 0) return;
   const int ns = (plan[b + 1] - f0) / (cu_q[b + 1] - c0);
   const int64_t i0 = f0 + (bt - c0) * ns;
   if (i0 + ns > max_items) return;
@@ -1535,7 +1685,7 @@ csa_status_t launch_paged(const AttnParams& p, const AttnMaps& m, cudaStream_t s
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
   const int grid = EPI == EPI_PARTIAL ? std::min(p.max_items, num_sms()) : (int)std::min<int64_t>(p.n_tok, num_sms());
-  e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p, m.q, m.kv, m.tok);
+  e = launch_pdl(kern, dim3(grid), dim3(attn_threads<KV, true>()), smem, st, p, m.q, m.kv, m.tok);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: launch failed: %s", cudaGetErrorString(e));
   return check_launch("csa_paged_attention");
 }
@@ -1855,6 +2005,19 @@ extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H,
   p.q = q; p.q_pos = q_pos; p.cu_q = cu_q; p.n_tok = n_tok; p.n_seq = n_seq; p.T = 1; p.H = H; p.n_split = 1;
   p.scale = scale; p.scale_log2 = scale * 1.4426950408889634f;
   p.sink = sink; p.out = out; p.out_bf16 = out_dtype == CSA_BF16;
+  p.max_items = paged_items(n_tok, n_seq);
+  // Chunks of several tokens a sequence share their rows on pairs of SMs.
+  const int64_t lim = (int64_t)1 << 31;
+  if (p.max_items == 0 && D == 512 && n_tok >= 2 * (int64_t)n_seq && kv_dtype == CSA_BF16 &&
+      (!tok_pages || (pair_page_size(tok_page_size) && n_tok_pages * tok_page_size < lim)) &&
+      (!kv_pages || (pair_page_size(kv_page_size) && n_kv_pages * kv_page_size < lim))) {
+    PairParams g{};
+    g.q = q; g.cu_q = cu_q; g.q_pos = q_pos; g.n_seq = n_seq; g.H = H; g.n_tok = n_tok;
+    g.rows[0] = tok_pages; g.pt[0] = p.pt2; g.cap[0] = p.cap2; g.W = W;
+    g.rows[1] = kv_pages; g.pt[1] = p.pt1; g.cap[1] = p.cap; g.m = p.m;
+    g.sink = sink; g.scale_log2 = p.scale_log2; g.out = out; g.out_bf16 = p.out_bf16;
+    return launch_paged_pair(g, stream);
+  }
   AttnMaps maps;
   memset(&maps, 0, sizeof(maps));
   if (!encode_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, D, n_tok * H, 64, kNQ, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -1871,7 +2034,6 @@ extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H,
       return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (tokens) failed");
     p.tma_tok = 1;
   }
-  p.max_items = paged_items(n_tok, n_seq);
   if (p.max_items == 0) return dispatch_paged<EPI_COMBINE>(p, maps, D, kv_dtype, stream);
   const size_t need = csa_paged_attention_workspace(n_tok, n_seq, H, D);
   if (!workspace || ws_bytes < need)
@@ -1886,7 +2048,7 @@ extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H,
   if (s != CSA_OK) return s;
   cudaError_t le = launch_pdl(paged_merge_kernel, dim3((unsigned)n_tok, (unsigned)((H * (D / 128) + 3) / 4)), dim3(128), 0,
                               stream, (const float*)p.O_part, (const float*)p.lse_part, (const int32_t*)p.plan, sink, cu_q,
-                              n_seq, p.max_items, H, D, out, (int)p.out_bf16);
+                              q_pos, n_seq, p.max_items, H, D, out, (int)p.out_bf16);
   if (le != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention(merge): launch failed: %s", cudaGetErrorString(le));
   return check_launch("csa_paged_attention(merge)");
 }

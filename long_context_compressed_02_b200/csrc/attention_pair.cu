@@ -1,0 +1,690 @@
+// Paged attention of prompt chunks on pairs of SMs (D = 512, bf16 rows).
+//
+// For a query row q (a head of a token) and the rows k_i that its token sees:
+//   out = sum_i e^{s q.k_i - M} k_i / (sum_i e^{s q.k_i - M} + e^{sink - M})
+//
+// Neighbouring tokens of a sequence see almost the same rows, so one load of a
+// row can serve several of them; what limits how many is TMEM, where an fp32
+// output row takes 512 columns.  A cluster of two CTAs works on 128 query rows
+// (two tokens of 64 heads, or more tokens of fewer heads): each CTA holds the
+// queries, probabilities and outputs of 64, and tcgen05.mma.cta_group::2 shares
+// the rows between the two tensor cores: each CTA loads half of every operand.
+//   S[128, 256 rows]  = Q K^T      M 128, N 256, K 512: CTA c loads rows 128 c ..
+//   O[128, 512]      += P V        M 128, 2 x N 256, K 256: CTA c loads dims 128 c ..
+//                                  of each 256
+// In TMEM an M = 128 pair accumulator has row l % 64 of a CTA in lane l, columns
+// [0, N/2) in lanes 0-63 and [N/2, N) in lanes 64-127: O takes 256 columns, two
+// S buffers 128 each, all 512.
+//
+// Operands stream through a ring of eight 16 KB stages, K as 128 rows x 64 dims,
+// V as 64 rows x 128 dims.  One thread issues all MMAs, in the order
+//   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
+// so that the softmax of tile i, which must wait for PV(i - 1) before it may
+// overwrite P and rescale O, runs under S(i + 1).
+//
+// Rows that some tokens of the pair see and others do not (the ends of a window,
+// the causal diagonal, an unfilled block) need care where they may hold NaN or
+// were never written: the logits of the tokens that do not see them are masked,
+// but their zero probability times a NaN is a NaN.  Such V blocks are not loaded
+// by TMA: loader warps copy the visible rows, with non-finite elements as zeros
+// (a token that does see the row gets its NaN from the logits), and zeros for
+// the others.
+#include <algorithm>
+#include <cstring>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+#include "common.cuh"
+#include "tc.cuh"
+#include "tmap.cuh"
+#include "paged.cuh"
+
+namespace csa {
+
+static __device__ uint32_t g_err_pair;
+
+uint32_t read_clear_err_pair() {
+  uint32_t v = 0, z = 0;
+  cudaMemcpyFromSymbol(&v, g_err_pair, sizeof(v));
+  cudaMemcpyToSymbol(g_err_pair, &z, sizeof(z));
+  return v;
+}
+
+namespace {
+
+constexpr int kD = 512;
+constexpr int kBlock = 64;                 // rows of a block: one page box, one slab of P
+constexpr int kTileBlocks = 4;             // 256 rows a tile
+constexpr int kStages = 8;
+constexpr uint32_t kStage = 16384;
+constexpr uint32_t kSlab = 8192;           // 64 rows x 128 bytes
+constexpr int kThreads = 320;              // warps 0-3 softmax, 4 TMA, 5 MMA / relay, 6-9 copies of V
+constexpr float kTau = 8.0f;               // lazy-rescale threshold (log2 units)
+constexpr uint32_t kSCol = 256;            // S buffers behind the 256 columns of O
+
+// ---------------------------------------------------------------- pair primitives
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrive on the barrier at this offset in CTA 0's shared memory.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+               "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}"
+               :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+// Bounded wait on a barrier of this CTA's; gives up after kWaitNs or once
+// another warp of the CTA has.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t start = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_ns();
+      if (start == 0) start = now;
+      else if (now - start > kWaitNs) break;
+    }
+  }
+  *abort_flag = 1;
+  atomicOr(&g_err_pair, DEV_ERR_TIMEOUT_MBAR);
+  return false;
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// Arrive on *bar in both CTAs when every MMA issued by this thread so far is done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
+  tmem_st16(taddr, v);
+  tmem_st16(taddr + 16, v + 16);
+}
+__device__ __forceinline__ float exp2_fast(float x) {     // flushes results below 2^-126 to zero
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+// Non-finite bf16 halves of a word become zeros.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  const uint32_t lo = (w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu;
+  const uint32_t hi = (w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u;
+  return lo | hi;
+}
+
+// The rows of a tile of tokens: blocks of 64 rows, raw rows first, then entries.
+struct Work {
+  int seq, tpc;                 // tokens per CTA
+  int64_t tok0, pos0;           // first token: row of the batch, position
+  int ntok;                     // tokens of the pair
+  int64_t wb0;                  // first block of raw rows
+  int nbw, nb;                  // blocks of raw rows, all blocks
+};
+
+// Rows [lo, hi) of source s (0 raw, 1 entries) that a query at position pos sees.
+__device__ __forceinline__ void seen(const PairParams& p, int s, int64_t pos, int64_t& lo, int64_t& hi) {
+  lo = hi = 0;
+  if (p.rows[s] == nullptr || pos < 0) return;
+  if (s == 0) {
+    hi = min(p.cap[0], pos + 1);
+    lo = p.W == 0 ? 0 : min(hi, max((int64_t)0, pos - p.W + 1));
+  } else {
+    hi = min(p.cap[1], (pos + 1) / p.m);
+  }
+}
+// Source and first row of block kb.
+__device__ __forceinline__ int block_at(const Work& w, int kb, int64_t& row) {
+  const int s = kb < w.nbw ? 0 : 1;
+  row = (s == 0 ? w.wb0 + kb : (int64_t)(kb - w.nbw)) * kBlock;
+  return s;
+}
+// Whether every token of the pair sees every row of block kb.
+__device__ __forceinline__ bool block_clean(const PairParams& p, const Work& w, int kb) {
+  int64_t row, lo0, hi0, lo1, hi1;
+  const int s = block_at(w, kb, row);
+  seen(p, s, w.pos0, lo0, hi0);
+  seen(p, s, w.pos0 + w.ntok - 1, lo1, hi1);
+  return row >= lo1 && row + kBlock <= hi0;
+}
+
+// Tile `x` of the batch, counted from the last tile of the last sequence (the
+// longest rows of a sequence come first, which leaves short tiles for the end).
+// Whole-warp call.
+__device__ __forceinline__ bool find_work(const PairParams& p, int64_t x, int lane, Work& w) {
+  w.tpc = max(1, 64 / p.H);
+  const int per = 2 * w.tpc;
+  for (int b0 = p.n_seq - 1; b0 >= 0; b0 -= 32) {
+    const int b = b0 - lane;
+    int len = 0;
+    if (b >= 0) len = max(0, p.cu_q[b + 1] - p.cu_q[b]);
+    const int tiles = (len + per - 1) / per;
+    int inc = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, x < inc);
+    if (hit == 0) {
+      x -= __shfl_sync(0xffffffffu, inc, 31);
+      continue;
+    }
+    const int l = __ffs(hit) - 1;
+    const int before = __shfl_sync(0xffffffffu, inc - tiles, l);
+    const int n = __shfl_sync(0xffffffffu, tiles, l);
+    len = __shfl_sync(0xffffffffu, len, l);
+    w.seq = b0 - l;
+    const int t = n - 1 - (int)(x - before);                 // tile of the sequence
+    w.tok0 = (int64_t)p.cu_q[w.seq] + (int64_t)t * per;
+    w.ntok = min(per, len - t * per);
+    w.pos0 = p.q_pos[w.seq] + (int64_t)t * per;
+    if (w.tok0 < 0 || w.tok0 + w.ntok > p.n_tok) return false;
+    const int64_t last = w.pos0 + w.ntok - 1;
+    int64_t lo, hi, h2, z;
+    seen(p, 0, max(w.pos0, (int64_t)0), lo, z);
+    seen(p, 0, last, z, hi);
+    seen(p, 1, last, z, h2);
+    w.wb0 = lo / kBlock;
+    w.nbw = hi > lo ? (int)((hi + kBlock - 1) / kBlock - w.wb0) : 0;
+    w.nb = w.nbw + (int)((h2 + kBlock - 1) / kBlock);
+    return true;
+  }
+  return false;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap map_q,
+            const __grid_constant__ CUtensorMap map_raw, const __grid_constant__ CUtensorMap map_ent) {
+  extern __shared__ uint8_t smem_raw[];
+  pdl_wait();
+  pdl_trigger();
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem;                                        // [8 slabs][64 rows][128 B]
+  uint8_t* sP = sQ + 8 * kSlab;                              // [4 slabs][64 rows][128 B]
+  uint8_t* sRing = sP + 4 * kSlab;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sRing + kStages * kStage);
+  uint64_t* full = bars;                                     // [8] this CTA's part of a stage is there
+  uint64_t* peer = full + kStages;                           // [8] CTA 0: CTA 1's part is there
+  uint64_t* empty = peer + kStages;                          // [8] the MMAs that read a stage are done
+  uint64_t* go = empty + kStages;                            // [8] the stage is the copying warps' to fill
+  uint64_t* q_full = go + kStages;
+  uint64_t* q_peer = q_full + 1;
+  uint64_t* s_full = q_peer + 1;                             // [2]
+  uint64_t* s_free = s_full + 2;                             // [2] CTA 0: read by the softmax of both CTAs
+  uint64_t* p_full = s_free + 2;                             // CTA 0: P and the rescaled O of both CTAs
+  uint64_t* pv_done = p_full + 1;
+  float* s_x = reinterpret_cast<float*>(pv_done + 1);        // [2][2][64] maxima / sums of the row halves
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_x + 256);
+  int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+  __shared__ Work s_work;
+  __shared__ int s_has;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t cta = cta_rank();
+  if (warp == 0) {
+    Work w;
+    const bool has = find_work(p, blockIdx.x >> 1, lane, w);
+    if (lane == 0) { s_work = w; s_has = has; }
+  }
+  if (tid == 32) {
+    for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&peer[i], 1); mbar_init(&empty[i], 1); mbar_init(&go[i], 1); }
+    mbar_init(q_full, 1); mbar_init(q_peer, 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 8); }
+    mbar_init(p_full, 8); mbar_init(pv_done, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (!s_has) return;                                        // the same in both CTAs
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(s_tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                            // barriers and TMEM of both CTAs are set up
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  volatile int* abort_flag = s_abort;
+  const Work w = s_work;
+  const int nt = (w.nb + kTileBlocks - 1) / kTileBlocks;     // tiles
+
+  // Stages in the order of the MMAs: K(0) K(1) V(0) K(2) V(1) ...  K(i) is 8
+  // stages (dims 64 j ..), V(i) two for each of its blocks (dims 256 j + 128 cta ..).
+  auto blocks_of = [&](int i) { return min(kTileBlocks, w.nb - kTileBlocks * i); };
+
+  if (warp == 4) {
+    // ============================ TMA producer
+    if (lane == 0) {
+      mbar_expect_tx(q_full, 8 * kSlab);
+      for (int s = 0; s < 8; ++s)
+        tma_load_2d(sQ + s * kSlab, &map_q, 64 * s, (int32_t)((w.tok0 + (int64_t)cta * w.tpc) * p.H), q_full);
+    }
+    uint32_t st = 0;                                         // stages so far
+    bool ok = true;
+    auto wait_empty = [&](uint32_t sl) {                     // one answer for the warp
+      if (lane == 0) ok = wait(&empty[sl], ((st / kStages) & 1) ^ 1, abort_flag);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      return ok;
+    };
+    // rows of the page store that hold a tile's blocks: lane kb * nsub + j for
+    // part j of block kb (pages of less than 64 rows make several boxes)
+    auto store_rows = [&](int i, int nsub, const PageTable& pt, int s, bool record) -> int32_t {
+      const int kb = lane / nsub, j = lane % nsub;           // at most 4 x 4
+      if (kb >= blocks_of(i)) return 0;
+      int64_t row;
+      if (block_at(w, kTileBlocks * i + kb, row) != s) return 0;
+      const int64_t g = page_row(pt, w.seq, row + j * (kBlock / nsub));
+      // A part without a page reads page 0.  It has no visible row, so its logits
+      // are masked and its V is not loaded here; or the table is wrong.
+      if (g < 0 && record && block_clean(p, w, kTileBlocks * i + kb)) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
+      return (int32_t)max((int64_t)0, g);
+    };
+    const int nsub[2] = {p.rows[0] ? max(1, kBlock >> p.pt[0].ps_log2) : 1, p.rows[1] ? max(1, kBlock >> p.pt[1].ps_log2) : 1};
+    auto box = [&](uint32_t dst, int s, int x, int32_t mine, int kb, uint64_t* bar) {
+      // 64 rows x 64 dims of block kb; called by the whole warp
+      const int rows = kBlock / nsub[s];
+      for (int j = 0; j < nsub[s]; ++j) {
+        const int32_t y = __shfl_sync(0xffffffffu, mine, kb * nsub[s] + j);
+        if (lane == 0)
+          tma_load_2d(reinterpret_cast<void*>(sRing + dst + j * rows * 128), s == 0 ? &map_raw : &map_ent, x, y, bar);
+      }
+    };
+    auto rows_of_tile = [&](int i, int32_t (&mine)[2], bool record) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) mine[s] = p.rows[s] ? store_rows(i, nsub[s], p.pt[s], s, record) : 0;
+    };
+    auto load_k = [&](int i) {
+      int32_t mine[2];
+      rows_of_tile(i, mine, false);
+      const int nbk = blocks_of(i);
+      for (int j = 0; j < 8 && ok; ++j, ++st) {
+        const uint32_t sl = st % kStages;
+        if (!wait_empty(sl)) break;
+        // blocks 2 cta, 2 cta + 1 of the tile; absent ones are not loaded (their logits are masked)
+        const int n = max(0, min(2, nbk - 2 * (int)cta));
+        if (lane == 0) {
+          if (n) mbar_expect_tx(&full[sl], n * kSlab);
+          else mbar_arrive(&full[sl]);
+        }
+        __syncwarp();
+        for (int h = 0; h < n; ++h) {
+          int64_t row;
+          const int kb = 2 * cta + h, s = block_at(w, kTileBlocks * i + kb, row);
+          box(sl * kStage + h * kSlab, s, 64 * j, s ? mine[1] : mine[0], kb, &full[sl]);
+        }
+      }
+    };
+    auto load_v = [&](int i) {
+      int32_t mine[2];
+      rows_of_tile(i, mine, true);
+      const int nbk = blocks_of(i);
+      for (int kb = 0; kb < nbk && ok; ++kb) {
+        int64_t row;
+        const int s = block_at(w, kTileBlocks * i + kb, row);
+        const bool clean = block_clean(p, w, kTileBlocks * i + kb);
+        for (int j = 0; j < 2 && ok; ++j, ++st) {
+          const uint32_t sl = st % kStages;
+          if (!wait_empty(sl)) break;
+          if (!clean) {                                      // the copying warps'
+            if (lane == 0) mbar_arrive(&go[sl]);
+            continue;
+          }
+          if (lane == 0) mbar_expect_tx(&full[sl], kStage);
+          __syncwarp();
+          for (int h = 0; h < 2; ++h)
+            box(sl * kStage + h * kSlab, s, 256 * j + 128 * cta + 64 * h, s ? mine[1] : mine[0], kb, &full[sl]);
+        }
+      }
+    };
+    if (nt > 0) load_k(0);
+    for (int i = 0; i < nt && ok; ++i) {
+      if (i + 1 < nt) load_k(i + 1);
+      if (ok) load_v(i);
+    }
+  } else if (warp >= 6) {
+    // ============================ copies of V blocks that not every token sees
+    const int lt = tid - 192;                                // 0 .. 127
+    // They see few of the stages, so the phase of `empty` tells them nothing (a
+    // parity is ambiguous two phases on): the producer, which sees all of them,
+    // hands a stage over through its `go`, once for each use.
+    uint32_t st = 0, uses = 0;                               // uses: bit sl, parity of the next use
+    bool ok = true;
+    if (nt > 0) st += 8;
+    for (int i = 0; i < nt && ok; ++i) {
+      if (i + 1 < nt) st += 8;
+      const int nbk = blocks_of(i);
+      for (int kb = 0; kb < nbk && ok; ++kb) {
+        if (block_clean(p, w, kTileBlocks * i + kb)) { st += 2; continue; }
+        int64_t row0, lo, z, hi;
+        const int s = block_at(w, kTileBlocks * i + kb, row0);
+        seen(p, s, max(w.pos0, (int64_t)0), lo, z);
+        seen(p, s, w.pos0 + w.ntok - 1, z, hi);              // rows [lo, hi): seen by some token
+        for (int j = 0; j < 2; ++j, ++st) {
+          const uint32_t sl = st % kStages;
+          // 64 rows x 128 dims: 16 pieces of 16 bytes a row, 16 lanes on a row
+          uint4 v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int r = u * 8 + (lt >> 4), c = lt & 15;
+            const int64_t row = row0 + r;
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (row >= lo && row < hi) {
+              const int64_t g = page_row(p.pt[s], w.seq, row);
+              if (g >= 0) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.rows[s]) + g * kD +
+                                                                     256 * j + 128 * cta + 8 * c));
+                v[u] = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+              } else if (c == 0) {
+                atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
+              }
+            }
+          }
+          ok = wait(&go[sl], (uses >> sl) & 1, abort_flag);
+          uses ^= 1u << sl;
+          if (named_bar_or(2, 128, !ok)) { ok = false; break; }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int r = u * 8 + (lt >> 4), c = lt & 15;
+            st_shared16(smem_u32(sRing) + sl * kStage + (c >> 3) * kSlab + swz128(r, c & 7), v[u]);
+          }
+          fence_proxy_async_smem();
+          named_bar_sync(2, 128);
+          if (lt == 0) mbar_arrive(&full[sl]);
+        }
+      }
+    }
+  } else if (warp == 5) {
+    if (cta == 1) {
+      // ============================ relay: tells CTA 0 what has landed here
+      if (lane == 0) {
+        bool ok = wait(q_full, 0, abort_flag);
+        if (ok) arrive_leader(q_peer);
+        uint32_t total = 0;
+        for (int i = 0; i < nt; ++i) total += 8 + 2 * blocks_of(i);
+        for (uint32_t st = 0; st < total && ok; ++st) {
+          ok = wait(&full[st % kStages], (st / kStages) & 1, abort_flag);
+          if (ok) arrive_leader(&peer[st % kStages]);
+        }
+      }
+    } else if (lane == 0) {
+      // ============================ MMA issuer
+      const uint32_t idesc_s = make_idesc(128, 256, 1, 1, 0, 0);
+      const uint32_t idesc_o = make_idesc(128, 256, 1, 1, 0, 1);
+      const uint64_t dQ = smem_desc(smem_u32(sQ), 16, 1024, SWZ_128B);
+      const uint64_t dP = smem_desc(smem_u32(sP), 16, 1024, SWZ_128B);
+      const uint64_t dK = smem_desc(smem_u32(sRing), 16, 1024, SWZ_128B);
+      const uint64_t dV = smem_desc(smem_u32(sRing), kSlab, 1024, SWZ_128B);
+      uint32_t st = 0;
+      bool ok = wait(q_full, 0, abort_flag) && wait(q_peer, 0, abort_flag);
+      auto stage = [&]() {
+        const uint32_t sl = st % kStages, ph = (st / kStages) & 1;
+        ok = ok && wait(&full[sl], ph, abort_flag) && wait(&peer[sl], ph, abort_flag);
+        tc_fence_after();
+        ++st;
+        return sl;
+      };
+      auto do_s = [&](int i) {
+        ok = ok && wait(&s_free[i & 1], ((i >> 1) & 1) ^ 1, abort_flag);
+        for (int j = 0; j < 8 && ok; ++j) {
+          const uint32_t sl = stage();
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_pair(tmem + kSCol + 128 * (i & 1), dQ + ((j * kSlab + k * 32) >> 4), dK + ((sl * kStage + k * 32) >> 4),
+                     idesc_s, (j | k) != 0);
+          commit_pair(&empty[sl]);
+        }
+        if (ok) commit_pair(&s_full[i & 1]);
+      };
+      auto do_pv = [&](int i) {
+        ok = ok && wait(p_full, i & 1, abort_flag);
+        const int nbk = blocks_of(i);
+        for (int kb = 0; kb < nbk && ok; ++kb)
+          for (int j = 0; j < 2 && ok; ++j) {
+            const uint32_t sl = stage();
+            if (!ok) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_pair(tmem + 128 * j, dP + ((kb * kSlab + k * 32) >> 4), dV + ((sl * kStage + k * 2048) >> 4), idesc_o,
+                       (i | kb | k) != 0);
+            commit_pair(&empty[sl]);
+          }
+        if (ok) commit_pair(pv_done);
+      };
+      if (nt > 0) do_s(0);
+      for (int i = 0; i < nt && ok; ++i) {
+        if (i + 1 < nt) do_s(i + 1);
+        if (ok) do_pv(i);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ============================ softmax and epilogue: lane tid of TMEM
+    const int r = tid & 63, half = tid >> 6;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const int tk = (int)cta * w.tpc + r / p.H;               // this row's token of the pair
+    const bool valid = r < w.tpc * p.H && tk < w.ntok && w.pos0 + tk >= 0;
+    const int64_t pos = valid ? w.pos0 + tk : -1;
+    int64_t lo[2], hi[2];
+    seen(p, 0, pos, lo[0], hi[0]);
+    seen(p, 1, pos, lo[1], hi[1]);
+    float m = -CUDART_INF_F, l = 0.f;
+    bool ok = true;
+    // After a wait that expired the warps only keep their barriers, so that none
+    // waits for another for ever.
+    for (int i = 0; i < nt; ++i) {
+      ok = __all_sync(0xffffffffu, ok && wait(&s_full[i & 1], (i >> 1) & 1, abort_flag));
+      tc_fence_after();
+      const uint32_t ts = tmem + lane_base + kSCol + 128 * (i & 1);
+      // which of this thread's 128 columns (blocks 2 half, 2 half + 1) the row's token sees
+      uint64_t see[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int kb = kTileBlocks * i + 2 * half + h;
+        see[h] = 0;
+        if (kb < w.nb) {
+          int64_t row;
+          const int s = block_at(w, kb, row);
+          const int64_t a = lo[s] - row, e = hi[s] - row;    // visible: [a, e) of the block
+          const uint64_t below = e >= 64 ? ~0ull : e <= 0 ? 0ull : (1ull << e) - 1;
+          const uint64_t from = a <= 0 ? ~0ull : a >= 64 ? 0ull : ~((1ull << a) - 1);
+          see[h] = below & from;
+        }
+      }
+      // pass 1: the maximum of the visible logits
+      float mx = -CUDART_INF_F;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (!ok) break;
+        float x[32];
+        tmem_ld32(ts + 32 * c, x);
+        tmem_wait_ld();
+        const uint32_t bits = (uint32_t)(see[c >> 1] >> (32 * (c & 1)));
+        if (bits == 0xffffffffu) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, x[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, (bits >> k) & 1u ? x[k] : -CUDART_INF_F);
+        }
+      }
+      float* sx = s_x + (i & 1) * 128;
+      sx[half * 64 + r] = mx;
+      if (named_bar_or(1, 128, !ok)) ok = false;
+      if (!ok) continue;
+      mx = fmaxf(sx[r], sx[64 + r]) * p.scale_log2;
+      // The maximum moves only when it grows by more than 2^kTau.
+      float alpha = 1.f;
+      if (mx > m + kTau) {
+        alpha = exp2f(m - mx);                               // 0 the first time
+        m = mx;
+      }
+      l *= alpha;
+      const float ref = m == -CUDART_INF_F ? 0.f : m;
+      // P and O are free once PV(i - 1) is done
+      if (i > 0) {
+        ok = __all_sync(0xffffffffu, wait(pv_done, (i - 1) & 1, abort_flag));
+        if (!ok) continue;
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float o[32];
+            tmem_ld32(tmem + lane_base + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= alpha;
+            tmem_st32(tmem + lane_base + 32 * c, o);
+          }
+          tmem_wait_st();
+        }
+      }
+      // pass 2: probabilities
+      const uint32_t pb = smem_u32(sP) + (2 * half) * kSlab;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float x[32];
+        tmem_ld32(ts + 32 * c, x);
+        tmem_wait_ld();
+        const uint32_t bits = (uint32_t)(see[c >> 1] >> (32 * (c & 1)));
+        if (bits == 0xffffffffu) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = exp2_fast(fmaf(x[k], p.scale_log2, -ref));
+        } else {
+          // a visible logit of -inf is a non-finite row's, whose V may read as zeros
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            x[k] = !((bits >> k) & 1u) ? 0.f : x[k] == -CUDART_INF_F ? CUDART_NAN_F : exp2_fast(fmaf(x[k], p.scale_log2, -ref));
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) l += x[k];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          st_shared16(pb + (c >> 1) * kSlab + swz128(r, 4 * (c & 1) + q),
+                      make_uint4(pack2(x[8 * q], x[8 * q + 1]), pack2(x[8 * q + 2], x[8 * q + 3]),
+                                 pack2(x[8 * q + 4], x[8 * q + 5]), pack2(x[8 * q + 6], x[8 * q + 7])));
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        arrive_leader(&s_free[i & 1]);
+        arrive_leader(p_full);
+      }
+    }
+    // ---------------- epilogue
+    {
+      float* sx = s_x + (nt & 1) * 128;
+      sx[half * 64 + r] = l;
+      named_bar_sync(1, 128);
+      l = sx[r] + sx[64 + r];
+      float coef = 0.f;
+      if (valid) {
+        const float sk = p.sink ? p.sink[r % p.H] * 1.4426950408889634f : -CUDART_INF_F;
+        if (l != 0.f || sk != -CUDART_INF_F) {               // a NaN sum passes
+          const float top = fmaxf(l != 0.f ? m : -CUDART_INF_F, sk);
+          const float e = l != 0.f ? exp2f(m - top) : 0.f;
+          coef = l != 0.f ? e / (e * l + exp2f(sk - top)) : 0.f;
+        }
+      }
+      if (nt > 0) ok = __all_sync(0xffffffffu, ok && wait(pv_done, (nt - 1) & 1, abort_flag));
+      if (ok) {
+        tc_fence_after();
+        const int64_t orow = ((w.tok0 + tk) * p.H + r % p.H) * kD;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          float o[32];
+          if (nt > 0) {
+            tmem_ld32(tmem + lane_base + 32 * c, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0.f;
+          }
+          if (valid) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = coef == 0.f ? 0.f : o[k] * coef;
+            // columns 128 j + 32 c' of O: dims 256 j + 128 half + 32 c'
+            const int d = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+            if (p.out_bf16) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow + d);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                dst[q] = make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
+                                    pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7]));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + d);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+  __syncwarp();
+  if (*abort_flag) {                                         // copies in flight land before shared memory goes
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 1000000ull) {}
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                            // neither CTA leaves while the other may reach it
+  if (warp == 5) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512));
+  }
+}
+
+}  // namespace
+
+csa_status_t launch_paged_pair(PairParams& p, cudaStream_t st) {
+  CUtensorMap maps[3];
+  memset(maps, 0, sizeof(maps));
+  if (!encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.q, kD, p.n_tok * p.H, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+    return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (queries) failed");
+  for (int s = 0; s < 2; ++s) {
+    if (!p.rows[s]) continue;
+    const int ps = 1 << p.pt[s].ps_log2;
+    if (!encode_2d(&maps[1 + s], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.rows[s], kD, p.pt[s].n_pages * ps, 64,
+                   std::min(ps, kBlock), CU_TENSOR_MAP_SWIZZLE_128B))
+      return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (pages) failed");
+  }
+  const size_t smem = 1024 + 12 * kSlab + kStages * kStage + (4 * kStages + 8) * 8 + 256 * 4 + 16;
+  cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
+  // Every sequence's last tile may be partly filled: an upper bound of the tiles
+  const int per = 2 * std::max(1, 64 / p.H);
+  const int64_t tiles = std::min(p.n_tok, p.n_tok / per + p.n_seq);
+  if (tiles > 0x3fffffff) return fail(CSA_ERR_UNSUPPORTED, "csa_paged_attention: too many tokens");
+  e = launch_pdl(pair_kernel, dim3((unsigned)(2 * tiles)), dim3(kThreads), smem, st, p, maps[0], maps[1], maps[2]);
+  if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: launch failed: %s", cudaGetErrorString(e));
+  return check_launch("csa_paged_attention");
+}
+
+}  // namespace csa

@@ -55,6 +55,7 @@ uint32_t read_clear_err_attention();
 uint32_t read_clear_err_proj();
 uint32_t read_clear_err_compress();
 uint32_t read_clear_err_rows();
+uint32_t read_clear_err_pair();
 uint32_t read_clear_err_selftest();
 
 }  // namespace csa

@@ -56,10 +56,13 @@ def page_rows(store, table_row, lo, hi):
 
 
 def e4m3_page_rows(codes, rope, scale, table_row, lo, hi):
-    """The rows as the attention reads them: codes * scale in float32, rounded to bf16, then the bf16 RoPE part."""
-    c = e4m3_decode(page_rows(codes, table_row, lo, hi)).astype(np.float32)
-    s = page_rows(scale, table_row, lo, hi).astype(np.float32)
-    return np.concatenate([bf16_round(c * s[:, None]), page_rows(rope, table_row, lo, hi).astype(np.float64)], -1)
+    """The rows as the attention reads them: codes * scale, and the RoPE part
+    divided by the scale, rounded to bf16 and multiplied by it again."""
+    c = e4m3_decode(page_rows(codes, table_row, lo, hi))
+    s = page_rows(scale, table_row, lo, hi).astype(np.float32)[:, None]
+    r = page_rows(rope, table_row, lo, hi).astype(np.float32)
+    turned = bf16_round(r * (np.float32(1) / s))
+    return np.concatenate([c, turned], -1) * s.astype(np.float64)
 
 
 __all__.append("e4m3_page_rows")

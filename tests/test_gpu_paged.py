@@ -349,6 +349,48 @@ def test_attention(csa, k):
     assert torch.equal(again[:m], out[:m])
 
 
+LONG = [
+    dict(lens=[81, 30], pos=[1500, 700], H=64, D=512, W=0),
+    dict(lens=[90], pos=[1900], H=64, D=512, W=0, ps=16),
+    dict(lens=[77, 1, 40], pos=[0, 3000, 1023], H=64, D=512, W=0, ps=32, sink=False),
+    dict(lens=[100], pos=[2000], H=64, D=512, m=2, W=300, ps=128),
+    dict(lens=[128], pos=[960], H=64, D=512, m=1, W=None, ps=64, sink=False),
+    dict(lens=[95], pos=[1200], H=16, D=512, W=0),
+    dict(lens=[120, 9], pos=[700, 900], H=33, D=512, m=4, W=511, ps=64),
+    dict(lens=[200], pos=[500], H=1, D=512, W=0, ps=64),
+    dict(lens=[100], pos=[800], H=64, D=128, W=0),
+    dict(lens=[99], pos=[4000], H=64, D=512, m=4, W=128, kind="e4m3"),
+    dict(lens=[2] * 60, pos=[37 * i for i in range(60)], H=64, D=512, W=0),
+]
+
+
+@pytest.mark.parametrize("k", range(len(LONG)))
+def test_attention_of_long_rows(csa, k):
+    """Chunks whose rows fill many tiles: first, last and odd tokens of every sequence."""
+    c = Case(seed=100 + k, pad=1, **LONG[k])
+    out = torch.full_like(c.q, 9.0)
+    csa.csa_paged_attention(c.q, c.cu, c.qp, out=out, **c.kw)
+    csa.check_device_error()
+    ends = {i for i in range(len(c.toks)) if i + 1 == len(c.toks) or c.toks[i][1] != c.toks[i + 1][1] or
+            i == 0 or c.toks[i][1] != c.toks[i - 1][1]}
+    c.check(out, only=sorted(ends | set(range(0, len(c.toks), 17)))[:24])
+    assert bool((out[-1] == 9.0).all()) and not bool(torch.isnan(out).any())
+    assert torch.equal(csa.csa_paged_attention(c.q, c.cu, c.qp, **c.kw)[:-1], out[:-1])
+
+
+def test_tokens_at_negative_positions_are_left_alone(csa):
+    for lens, H, D in (([4], 64, 512), ([90], 64, 512), ([90], 8, 128)):
+        c = Case(lens=lens, pos=[0], H=H, D=D, W=0)
+        out = torch.full_like(c.q, 3.0)
+        csa.csa_paged_attention(c.q, c.cu, torch.tensor([-2], device="cuda"), out=out, **c.kw)
+        csa.check_device_error()
+        assert bool((out[:2] == 3.0).all())
+        ref = csa.csa_paged_attention(c.q[2:].contiguous(), torch.tensor([0, lens[0] - 2], dtype=torch.int32, device="cuda"),
+                                      torch.tensor([0], device="cuda"), **c.kw)
+        tol = 2.0 ** -6 * ref.float().abs().max()               # another split of the rows: other roundings of P
+        assert bool(((out[2:].float() - ref.float()).abs() <= tol).all())
+
+
 def test_rows_out_of_sight_do_not_matter(csa):
     """A later token's NaN row reaches that token and those after it only, in decode-sized and chunk-sized batches."""
     for lens, H, D in (([12], 64, 512), ([110], 64, 512), ([110], 8, 128)):
