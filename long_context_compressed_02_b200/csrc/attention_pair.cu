@@ -16,8 +16,8 @@
 // [0, N/2) in lanes 0-63 and [N/2, N) in lanes 64-127: O takes 256 columns, two
 // S buffers 128 each, all 512.
 //
-// Operands stream through a ring of eight 16 KB stages, K as 128 rows x 64 dims,
-// V as 64 rows x 128 dims.  One thread issues all MMAs, in the order
+// Operands stream through a ring of four 32 KB stages of 8 MMAs, K as 128 rows x
+// 128 dims, V as 64 rows x 256 dims.  One thread issues all MMAs, in the order
 //   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
 // so that the softmax of tile i, which must wait for PV(i - 1) before it may
 // overwrite P and rescale O, runs under S(i + 1).
@@ -54,10 +54,11 @@ namespace {
 constexpr int kD = 512;
 constexpr int kBlock = 64;                 // rows of a block: one page box, one slab of P
 constexpr int kTileBlocks = 4;             // 256 rows a tile
-constexpr int kStages = 8;
-constexpr uint32_t kStage = 16384;
+constexpr int kStages = 4;
+constexpr uint32_t kStage = 32768;         // K: [2 x 64 dims][128 rows], V: [4 x 64 dims][64 rows]
+constexpr int kKStages = 4;                // stages of a tile's K; its V has one for each block
 constexpr uint32_t kSlab = 8192;           // 64 rows x 128 bytes
-constexpr int kThreads = 320;              // warps 0-3 softmax, 4 TMA, 5 MMA / relay, 6-9 copies of V
+constexpr int kThreads = 320;              // warps 0-3 softmax, 4 TMA, 5 MMA (CTA 0), 6-9 copies of V
 constexpr float kTau = 8.0f;               // lazy-rescale threshold (log2 units)
 constexpr uint32_t kSCol = 256;            // S buffers behind the 256 columns of O
 
@@ -70,26 +71,22 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrive on the barrier at this offset in CTA 0's shared memory.
+// Arrive on the barrier at this offset in CTA 0's shared memory.  The barriers
+// of a pair announce shared memory that only the tensor cores read (written by
+// TMA, or by threads that fenced it for the async proxy), so arrivals release and
+// waits acquire at CTA scope: a cluster-scope release costs 1,000 cycles and more
+// each, which 16 stages a tile paid one after another (20,000 cycles a tile).
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-               "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}"
+               "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}"
                :: "r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-  return ok != 0;
 }
 // Bounded wait on a barrier of this CTA's; gives up after kWaitNs or once
 // another warp of the CTA has.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   uint64_t start = 0;
   for (uint32_t i = 1;; ++i) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 0) {
       if (*abort_flag) return false;
       const uint64_t now = global_ns();
@@ -100,6 +97,20 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   *abort_flag = 1;
   atomicOr(&g_err_pair, DEV_ERR_TIMEOUT_MBAR);
   return false;
+}
+// The same, announcing `bytes` of copies that complete there.
+__device__ __forceinline__ void expect_leader(uint64_t* bar, uint32_t bytes) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+               "mbarrier.arrive.expect_tx.shared::cluster.b64 _, [a], %1;\n\t}"
+               :: "r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// Tiled copy into this CTA's shared memory that completes on CTA 0's barrier.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint64_t* bar) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, 0;\n\t"
+               "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+               " [%0], [%1, {%2, %3}], [a];\n\t}"
+               :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -141,6 +152,8 @@ struct Work {
   int ntok;                     // tokens of the pair
   int64_t wb0;                  // first block of raw rows
   int nbw, nb;                  // blocks of raw rows, all blocks
+  int64_t any_lo[2], any_hi[2]; // rows of each source that some token sees ...
+  int64_t all_lo[2], all_hi[2]; // ... and that every token sees
 };
 
 // Rows [lo, hi) of source s (0 raw, 1 entries) that a query at position pos sees.
@@ -161,12 +174,10 @@ __device__ __forceinline__ int block_at(const Work& w, int kb, int64_t& row) {
   return s;
 }
 // Whether every token of the pair sees every row of block kb.
-__device__ __forceinline__ bool block_clean(const PairParams& p, const Work& w, int kb) {
-  int64_t row, lo0, hi0, lo1, hi1;
+__device__ __forceinline__ bool block_clean(const Work& w, int kb) {
+  int64_t row;
   const int s = block_at(w, kb, row);
-  seen(p, s, w.pos0, lo0, hi0);
-  seen(p, s, w.pos0 + w.ntok - 1, lo1, hi1);
-  return row >= lo1 && row + kBlock <= hi0;
+  return row >= (s ? w.all_lo[1] : w.all_lo[0]) && row + kBlock <= (s ? w.all_hi[1] : w.all_hi[0]);
 }
 
 // Tile `x` of the batch, counted from the last tile of the last sequence (the
@@ -202,13 +213,17 @@ __device__ __forceinline__ bool find_work(const PairParams& p, int64_t x, int la
     w.pos0 = p.q_pos[w.seq] + (int64_t)t * per;
     if (w.tok0 < 0 || w.tok0 + w.ntok > p.n_tok) return false;
     const int64_t last = w.pos0 + w.ntok - 1;
-    int64_t lo, hi, h2, z;
-    seen(p, 0, max(w.pos0, (int64_t)0), lo, z);
-    seen(p, 0, last, z, hi);
-    seen(p, 1, last, z, h2);
-    w.wb0 = lo / kBlock;
-    w.nbw = hi > lo ? (int)((hi + kBlock - 1) / kBlock - w.wb0) : 0;
-    w.nb = w.nbw + (int)((h2 + kBlock - 1) / kBlock);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      int64_t z;
+      seen(p, s, max(w.pos0, (int64_t)0), w.any_lo[s], z);
+      seen(p, s, last, z, w.any_hi[s]);
+      seen(p, s, last, w.all_lo[s], z);
+      seen(p, s, w.pos0, z, w.all_hi[s]);
+    }
+    w.wb0 = w.any_lo[0] / kBlock;
+    w.nbw = w.any_hi[0] > w.any_lo[0] ? (int)((w.any_hi[0] + kBlock - 1) / kBlock - w.wb0) : 0;
+    w.nb = w.nbw + (int)((w.any_hi[1] + kBlock - 1) / kBlock);
     return true;
   }
   return false;
@@ -225,13 +240,11 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
   uint8_t* sP = sQ + 8 * kSlab;                              // [4 slabs][64 rows][128 B]
   uint8_t* sRing = sP + 4 * kSlab;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sRing + kStages * kStage);
-  uint64_t* full = bars;                                     // [8] this CTA's part of a stage is there
-  uint64_t* peer = full + kStages;                           // [8] CTA 0: CTA 1's part is there
-  uint64_t* empty = peer + kStages;                          // [8] the MMAs that read a stage are done
-  uint64_t* go = empty + kStages;                            // [8] the stage is the copying warps' to fill
-  uint64_t* q_full = go + kStages;
-  uint64_t* q_peer = q_full + 1;
-  uint64_t* s_full = q_peer + 1;                             // [2]
+  uint64_t* full = bars;                                     // [4] CTA 0: a stage's parts in both CTAs are there
+  uint64_t* empty = full + kStages;                          // [4] the MMAs that read a stage are done
+  uint64_t* go = empty + kStages;                            // [4] the stage is the copying warps' to fill
+  uint64_t* q_full = go + kStages;                           // CTA 0: the queries of both CTAs
+  uint64_t* s_full = q_full + 1;                             // [2]
   uint64_t* s_free = s_full + 2;                             // [2] CTA 0: read by the softmax of both CTAs
   uint64_t* p_full = s_free + 2;                             // CTA 0: P and the rescaled O of both CTAs
   uint64_t* pv_done = p_full + 1;
@@ -249,8 +262,8 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
     if (lane == 0) { s_work = w; s_has = has; }
   }
   if (tid == 32) {
-    for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&peer[i], 1); mbar_init(&empty[i], 1); mbar_init(&go[i], 1); }
-    mbar_init(q_full, 1); mbar_init(q_peer, 1);
+    for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); mbar_init(&go[i], 1); }
+    mbar_init(q_full, 2);
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 8); }
     mbar_init(p_full, 8); mbar_init(pv_done, 1);
     *s_abort = 0;
@@ -271,98 +284,93 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
   const Work w = s_work;
   const int nt = (w.nb + kTileBlocks - 1) / kTileBlocks;     // tiles
 
-  // Stages in the order of the MMAs: K(0) K(1) V(0) K(2) V(1) ...  K(i) is 8
-  // stages (dims 64 j ..), V(i) two for each of its blocks (dims 256 j + 128 cta ..).
+  // Stages in the order of the MMAs: K(0) K(1) V(0) K(2) V(1) ...  K(i) is 4
+  // stages (dims 128 d ..), V(i) one for each of its blocks (the dims
+  // 256 j + 128 cta .. of j = 0, 1).  A stage has one arrival from each CTA.
   auto blocks_of = [&](int i) { return min(kTileBlocks, w.nb - kTileBlocks * i); };
 
   if (warp == 4) {
     // ============================ TMA producer
     if (lane == 0) {
-      mbar_expect_tx(q_full, 8 * kSlab);
+      expect_leader(q_full, 8 * kSlab);
       for (int s = 0; s < 8; ++s)
-        tma_load_2d(sQ + s * kSlab, &map_q, 64 * s, (int32_t)((w.tok0 + (int64_t)cta * w.tpc) * p.H), q_full);
+        tma_load_pair(sQ + s * kSlab, &map_q, 64 * s, (int32_t)((w.tok0 + (int64_t)cta * w.tpc) * p.H), q_full);
     }
+    // Lane 4 kb + j has part j of block kb of a tile: pages of less than 64 rows
+    // make several boxes of a block.  It looks its row of the page store up a tile
+    // ahead and issues the copies of its part itself.
     uint32_t st = 0;                                         // stages so far
     bool ok = true;
+    const int kb = lane >> 2, j = lane & 3;
+    struct Part { int32_t y; int s, rows; bool on; };        // first row, source, rows; whether there is one
+    auto part_of = [&](int i) {
+      Part t{0, 0, kBlock, false};
+      if (i < nt && kb < blocks_of(i)) {
+        int64_t row;
+        t.s = block_at(w, kTileBlocks * i + kb, row);
+        const PageTable& pt = t.s ? p.pt[1] : p.pt[0];
+        t.rows = min(kBlock, 1 << pt.ps_log2);
+        t.on = j * t.rows < kBlock;
+        if (t.on) {
+          const int64_t g = page_row(pt, w.seq, row + j * t.rows);
+          // A part without a page reads page 0.  It has no visible row, so its logits
+          // are masked and its V is not loaded here; or the table is wrong.
+          if (g < 0 && block_clean(w, kTileBlocks * i + kb)) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
+          t.y = (int32_t)max((int64_t)0, g);
+        }
+      }
+      return t;
+    };
     auto wait_empty = [&](uint32_t sl) {                     // one answer for the warp
-      if (lane == 0) ok = wait(&empty[sl], ((st / kStages) & 1) ^ 1, abort_flag);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = __all_sync(0xffffffffu, wait(&empty[sl], ((st / kStages) & 1) ^ 1, abort_flag));
       return ok;
     };
-    // rows of the page store that hold a tile's blocks: lane kb * nsub + j for
-    // part j of block kb (pages of less than 64 rows make several boxes)
-    auto store_rows = [&](int i, int nsub, const PageTable& pt, int s, bool record) -> int32_t {
-      const int kb = lane / nsub, j = lane % nsub;           // at most 4 x 4
-      if (kb >= blocks_of(i)) return 0;
-      int64_t row;
-      if (block_at(w, kTileBlocks * i + kb, row) != s) return 0;
-      const int64_t g = page_row(pt, w.seq, row + j * (kBlock / nsub));
-      // A part without a page reads page 0.  It has no visible row, so its logits
-      // are masked and its V is not loaded here; or the table is wrong.
-      if (g < 0 && record && block_clean(p, w, kTileBlocks * i + kb)) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
-      return (int32_t)max((int64_t)0, g);
-    };
-    const int nsub[2] = {p.rows[0] ? max(1, kBlock >> p.pt[0].ps_log2) : 1, p.rows[1] ? max(1, kBlock >> p.pt[1].ps_log2) : 1};
-    auto box = [&](uint32_t dst, int s, int x, int32_t mine, int kb, uint64_t* bar) {
-      // 64 rows x 64 dims of block kb; called by the whole warp
-      const int rows = kBlock / nsub[s];
-      for (int j = 0; j < nsub[s]; ++j) {
-        const int32_t y = __shfl_sync(0xffffffffu, mine, kb * nsub[s] + j);
-        if (lane == 0)
-          tma_load_2d(reinterpret_cast<void*>(sRing + dst + j * rows * 128), s == 0 ? &map_raw : &map_ent, x, y, bar);
-      }
-    };
-    auto rows_of_tile = [&](int i, int32_t (&mine)[2], bool record) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) mine[s] = p.rows[s] ? store_rows(i, nsub[s], p.pt[s], s, record) : 0;
-    };
-    auto load_k = [&](int i) {
-      int32_t mine[2];
-      rows_of_tile(i, mine, false);
-      const int nbk = blocks_of(i);
-      for (int j = 0; j < 8 && ok; ++j, ++st) {
+    auto load_k = [&](int i, const Part& t) {
+      // blocks 2 cta, 2 cta + 1 of the tile; absent ones are not loaded (their logits are masked)
+      const int n = max(0, min(2, blocks_of(i) - 2 * (int)cta));
+      const bool mine = t.on && (kb >> 1) == (int)cta;
+      const CUtensorMap* map = t.s ? &map_ent : &map_raw;
+      for (int d = 0; d < kKStages; ++d, ++st) {
         const uint32_t sl = st % kStages;
         if (!wait_empty(sl)) break;
-        // blocks 2 cta, 2 cta + 1 of the tile; absent ones are not loaded (their logits are masked)
-        const int n = max(0, min(2, nbk - 2 * (int)cta));
         if (lane == 0) {
-          if (n) mbar_expect_tx(&full[sl], n * kSlab);
-          else mbar_arrive(&full[sl]);
+          if (n) expect_leader(&full[sl], n * 2 * kSlab);
+          else arrive_leader(&full[sl]);
         }
-        __syncwarp();
-        for (int h = 0; h < n; ++h) {
-          int64_t row;
-          const int kb = 2 * cta + h, s = block_at(w, kTileBlocks * i + kb, row);
-          box(sl * kStage + h * kSlab, s, 64 * j, s ? mine[1] : mine[0], kb, &full[sl]);
+        if (mine) {
+          uint8_t* dst = sRing + sl * kStage + (kb & 1) * kSlab + j * t.rows * 128;
+          tma_load_pair(dst, map, 128 * d, t.y, &full[sl]);
+          tma_load_pair(dst + 2 * kSlab, map, 128 * d + 64, t.y, &full[sl]);
         }
       }
     };
-    auto load_v = [&](int i) {
-      int32_t mine[2];
-      rows_of_tile(i, mine, true);
+    auto load_v = [&](int i, const Part& t) {
+      const CUtensorMap* map = t.s ? &map_ent : &map_raw;
       const int nbk = blocks_of(i);
-      for (int kb = 0; kb < nbk && ok; ++kb) {
-        int64_t row;
-        const int s = block_at(w, kTileBlocks * i + kb, row);
-        const bool clean = block_clean(p, w, kTileBlocks * i + kb);
-        for (int j = 0; j < 2 && ok; ++j, ++st) {
-          const uint32_t sl = st % kStages;
-          if (!wait_empty(sl)) break;
-          if (!clean) {                                      // the copying warps'
-            if (lane == 0) mbar_arrive(&go[sl]);
-            continue;
-          }
-          if (lane == 0) mbar_expect_tx(&full[sl], kStage);
-          __syncwarp();
-          for (int h = 0; h < 2; ++h)
-            box(sl * kStage + h * kSlab, s, 256 * j + 128 * cta + 64 * h, s ? mine[1] : mine[0], kb, &full[sl]);
+      for (int v = 0; v < nbk && ok; ++v, ++st) {
+        const uint32_t sl = st % kStages;
+        if (!wait_empty(sl)) break;
+        if (!block_clean(w, kTileBlocks * i + v)) {          // the copying warps'
+          if (lane == 0) mbar_arrive(&go[sl]);
+          continue;
+        }
+        if (lane == 0) expect_leader(&full[sl], kStage);
+        if (t.on && kb == v) {
+          uint8_t* dst = sRing + sl * kStage + j * t.rows * 128;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            tma_load_pair(dst + h * kSlab, map, 256 * (h >> 1) + 128 * (int)cta + 64 * (h & 1), t.y, &full[sl]);
         }
       }
     };
-    if (nt > 0) load_k(0);
+    Part cur = part_of(0), next = part_of(1);
+    if (nt > 0) load_k(0, cur);
     for (int i = 0; i < nt && ok; ++i) {
-      if (i + 1 < nt) load_k(i + 1);
-      if (ok) load_v(i);
+      const Part after = part_of(i + 2);
+      if (i + 1 < nt) load_k(i + 1, next);
+      if (ok) load_v(i, cur);
+      cur = next;
+      next = after;
     }
   } else if (warp >= 6) {
     // ============================ copies of V blocks that not every token sees
@@ -372,18 +380,20 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
     // hands a stage over through its `go`, once for each use.
     uint32_t st = 0, uses = 0;                               // uses: bit sl, parity of the next use
     bool ok = true;
-    if (nt > 0) st += 8;
+    if (nt > 0) st += kKStages;
     for (int i = 0; i < nt && ok; ++i) {
-      if (i + 1 < nt) st += 8;
+      if (i + 1 < nt) st += kKStages;
       const int nbk = blocks_of(i);
-      for (int kb = 0; kb < nbk && ok; ++kb) {
-        if (block_clean(p, w, kTileBlocks * i + kb)) { st += 2; continue; }
-        int64_t row0, lo, z, hi;
+      for (int kb = 0; kb < nbk && ok; ++kb, ++st) {
+        if (block_clean(w, kTileBlocks * i + kb)) continue;
+        int64_t row0;
         const int s = block_at(w, kTileBlocks * i + kb, row0);
-        seen(p, s, max(w.pos0, (int64_t)0), lo, z);
-        seen(p, s, w.pos0 + w.ntok - 1, z, hi);              // rows [lo, hi): seen by some token
-        for (int j = 0; j < 2; ++j, ++st) {
-          const uint32_t sl = st % kStages;
+        const PageTable& pt = s ? p.pt[1] : p.pt[0];
+        const __nv_bfloat16* store = static_cast<const __nv_bfloat16*>(s ? p.rows[1] : p.rows[0]);
+        const int64_t lo = s ? w.any_lo[1] : w.any_lo[0], hi = s ? w.any_hi[1] : w.any_hi[0];
+        const uint32_t sl = st % kStages;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
           // 64 rows x 128 dims: 16 pieces of 16 bytes a row, 16 lanes on a row
           uint4 v[8];
 #pragma unroll
@@ -392,44 +402,32 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
             const int64_t row = row0 + r;
             v[u] = make_uint4(0, 0, 0, 0);
             if (row >= lo && row < hi) {
-              const int64_t g = page_row(p.pt[s], w.seq, row);
-              if (g >= 0) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.rows[s]) + g * kD +
-                                                                     256 * j + 128 * cta + 8 * c));
-                v[u] = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
-              } else if (c == 0) {
-                atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
-              }
+              const int64_t g = page_row(pt, w.seq, row);
+              if (g >= 0) v[u] = __ldg(reinterpret_cast<const uint4*>(store + g * kD + 256 * j + 128 * cta + 8 * c));
+              else if (c == 0) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
             }
           }
-          ok = wait(&go[sl], (uses >> sl) & 1, abort_flag);
-          uses ^= 1u << sl;
-          if (named_bar_or(2, 128, !ok)) { ok = false; break; }
+          if (j == 0) {
+            ok = wait(&go[sl], (uses >> sl) & 1, abort_flag);
+            uses ^= 1u << sl;
+            if (named_bar_or(2, 128, !ok)) ok = false;       // one answer for the four warps
+            if (!ok) break;
+          }
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             const int r = u * 8 + (lt >> 4), c = lt & 15;
-            st_shared16(smem_u32(sRing) + sl * kStage + (c >> 3) * kSlab + swz128(r, c & 7), v[u]);
+            v[u] = make_uint4(finite2(v[u].x), finite2(v[u].y), finite2(v[u].z), finite2(v[u].w));
+            st_shared16(smem_u32(sRing) + sl * kStage + (2 * j + (c >> 3)) * kSlab + swz128(r, c & 7), v[u]);
           }
-          fence_proxy_async_smem();
-          named_bar_sync(2, 128);
-          if (lt == 0) mbar_arrive(&full[sl]);
         }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        named_bar_sync(2, 128);
+        if (lt == 0) arrive_leader(&full[sl]);
       }
     }
   } else if (warp == 5) {
-    if (cta == 1) {
-      // ============================ relay: tells CTA 0 what has landed here
-      if (lane == 0) {
-        bool ok = wait(q_full, 0, abort_flag);
-        if (ok) arrive_leader(q_peer);
-        uint32_t total = 0;
-        for (int i = 0; i < nt; ++i) total += 8 + 2 * blocks_of(i);
-        for (uint32_t st = 0; st < total && ok; ++st) {
-          ok = wait(&full[st % kStages], (st / kStages) & 1, abort_flag);
-          if (ok) arrive_leader(&peer[st % kStages]);
-        }
-      }
-    } else if (lane == 0) {
+    if (cta == 0 && lane == 0) {
       // ============================ MMA issuer
       const uint32_t idesc_s = make_idesc(128, 256, 1, 1, 0, 0);
       const uint32_t idesc_o = make_idesc(128, 256, 1, 1, 0, 1);
@@ -438,23 +436,23 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
       const uint64_t dK = smem_desc(smem_u32(sRing), 16, 1024, SWZ_128B);
       const uint64_t dV = smem_desc(smem_u32(sRing), kSlab, 1024, SWZ_128B);
       uint32_t st = 0;
-      bool ok = wait(q_full, 0, abort_flag) && wait(q_peer, 0, abort_flag);
+      bool ok = wait(q_full, 0, abort_flag);
       auto stage = [&]() {
         const uint32_t sl = st % kStages, ph = (st / kStages) & 1;
-        ok = ok && wait(&full[sl], ph, abort_flag) && wait(&peer[sl], ph, abort_flag);
+        ok = ok && wait(&full[sl], ph, abort_flag);
         tc_fence_after();
         ++st;
         return sl;
       };
       auto do_s = [&](int i) {
         ok = ok && wait(&s_free[i & 1], ((i >> 1) & 1) ^ 1, abort_flag);
-        for (int j = 0; j < 8 && ok; ++j) {
+        for (int d = 0; d < kKStages && ok; ++d) {
           const uint32_t sl = stage();
           if (!ok) break;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_pair(tmem + kSCol + 128 * (i & 1), dQ + ((j * kSlab + k * 32) >> 4), dK + ((sl * kStage + k * 32) >> 4),
-                     idesc_s, (j | k) != 0);
+          for (int k = 0; k < 8; ++k)
+            mma_pair(tmem + kSCol + 128 * (i & 1), dQ + (((2 * d + (k >> 2)) * kSlab + (k & 3) * 32) >> 4),
+                     dK + ((sl * kStage + (k >> 2) * 2 * kSlab + (k & 3) * 32) >> 4), idesc_s, (d | k) != 0);
           commit_pair(&empty[sl]);
         }
         if (ok) commit_pair(&s_full[i & 1]);
@@ -462,16 +460,16 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
       auto do_pv = [&](int i) {
         ok = ok && wait(p_full, i & 1, abort_flag);
         const int nbk = blocks_of(i);
-        for (int kb = 0; kb < nbk && ok; ++kb)
-          for (int j = 0; j < 2 && ok; ++j) {
-            const uint32_t sl = stage();
-            if (!ok) break;
+        for (int kb = 0; kb < nbk && ok; ++kb) {
+          const uint32_t sl = stage();
+          if (!ok) break;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_pair(tmem + 128 * j, dP + ((kb * kSlab + k * 32) >> 4), dV + ((sl * kStage + k * 2048) >> 4), idesc_o,
-                       (i | kb | k) != 0);
-            commit_pair(&empty[sl]);
-          }
+          for (int k = 0; k < 8; ++k)
+            mma_pair(tmem + 128 * (k >> 2), dP + ((kb * kSlab + (k & 3) * 32) >> 4),
+                     dV + ((sl * kStage + (k >> 2) * 2 * kSlab + (k & 3) * 2048) >> 4), idesc_o,
+                     (i | kb | (k & 3)) != 0);
+          commit_pair(&empty[sl]);
+        }
         if (ok) commit_pair(pv_done);
       };
       if (nt > 0) do_s(0);
@@ -675,7 +673,7 @@ csa_status_t launch_paged_pair(PairParams& p, cudaStream_t st) {
                    std::min(ps, kBlock), CU_TENSOR_MAP_SWIZZLE_128B))
       return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (pages) failed");
   }
-  const size_t smem = 1024 + 12 * kSlab + kStages * kStage + (4 * kStages + 8) * 8 + 256 * 4 + 16;
+  const size_t smem = 1024 + 12 * kSlab + kStages * kStage + (3 * kStages + 7) * 8 + 256 * 4 + 16;
   cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
   // Every sequence's last tile may be partly filled: an upper bound of the tiles
