@@ -479,6 +479,7 @@ csa_status_t csa_paged_append(const void* rows, csa_dtype_t in_dtype, int64_t ro
  * The token's own raw row must be in its page before the call
  * (csa_paged_append).  A token that sees no row yields 0.
  *   q [n_tok, H, D] BF16, normalised and rotated; H in [1, 64]; D 128 or 512.
+ *   scale > 0.
  *   tok_pages [n_tok_pages, tok_page_size, D] BF16.
  *   kv_pages [n_kv_pages, kv_page_size, D] BF16, or E4M3 with kv_rope and
  *     kv_scale (the row format of csa_paged_append).

@@ -1975,6 +1975,7 @@ extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H,
   CSA_REQUIRE(out_dtype == CSA_F32 || out_dtype == CSA_BF16, "csa_paged_attention: out_dtype must be F32 or BF16");
   CSA_REQUIRE(tok_pages || kv_pages, "csa_paged_attention: token pages or entry pages required");
   CSA_REQUIRE(W >= 0, "csa_paged_attention: W must not be negative");
+  CSA_REQUIRE(scale > 0.f && scale <= 3.0e38f, "csa_paged_attention: scale must be positive and finite");
   if (n_tok == 0 || n_seq == 0) return CSA_OK;
   if (n_tok * H >= (int64_t)1 << 31) return fail(CSA_ERR_UNSUPPORTED, "csa_paged_attention: n_tok * H must be below 2^31");
   CSA_REQUIRE(q && out && aligned16(q) && aligned16(out), "csa_paged_attention: q / out must be non-null and 16-byte aligned");

@@ -17,10 +17,17 @@
 // S buffers 128 each, all 512.
 //
 // Operands stream through a ring of four 32 KB stages of 8 MMAs, K as 128 rows x
-// 128 dims, V as 64 rows x 256 dims.  One thread issues all MMAs, in the order
-//   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
-// so that the softmax of tile i, which must wait for PV(i - 1) before it may
-// overwrite P and rescale O, runs under S(i + 1).
+// 128 dims, V as 64 rows x 256 dims.  A thread that issues MMAs loses about 270
+// cycles at every wait (its polls queue behind its MMAs, and the tensor pipe runs
+// dry meanwhile), so S and PV have an issuer each, on different schedulers, and
+// the stages of PV(t) and S(t + 2) alternate in the ring: each issuer's waits are
+// covered by the other's MMAs.  The softmax of tile t + 1 runs under both, keeps
+// its probabilities in registers, and writes them as soon as PV(t) has read P.
+//
+// Clusters are persistent and take every n-th pair of token groups (an item).
+// Tiles follow one another over the items, and one warp looks the items up ahead
+// of the others, so the next queries, keys and logits are there while an item's
+// output is written.
 //
 // Rows that some tokens of the pair see and others do not (the ends of a window,
 // the causal diagonal, an unfilled block) need care where they may hold NaN or
@@ -58,9 +65,10 @@ constexpr int kStages = 4;
 constexpr uint32_t kStage = 32768;         // K: [2 x 64 dims][128 rows], V: [4 x 64 dims][64 rows]
 constexpr int kKStages = 4;                // stages of a tile's K; its V has one for each block
 constexpr uint32_t kSlab = 8192;           // 64 rows x 128 bytes
-constexpr int kThreads = 320;              // warps 0-3 softmax, 4 TMA, 5 MMA (CTA 0), 6-9 copies of V
+constexpr int kThreads = 384;              // warps 0-3 softmax, 4 TMA, 5 S and 6 PV (CTA 0), 7 items, 8-11 copies of V
 constexpr float kTau = 8.0f;               // lazy-rescale threshold (log2 units)
 constexpr uint32_t kSCol = 256;            // S buffers behind the 256 columns of O
+constexpr int kItems = 4;                  // items that are looked up ahead
 
 // ---------------------------------------------------------------- pair primitives
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -112,6 +120,10 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
                :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
                : "memory");
 }
+// The same for a whole warp, with one answer.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait(bar, parity, abort_flag));
+}
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
@@ -124,10 +136,6 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 }
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
-  tmem_st16(taddr, v);
-  tmem_st16(taddr + 16, v + 16);
 }
 __device__ __forceinline__ float exp2_fast(float x) {     // flushes results below 2^-126 to zero
   float y;
@@ -147,6 +155,7 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
 
 // The rows of a tile of tokens: blocks of 64 rows, raw rows first, then entries.
 struct Work {
+  int has;                      // 0: no item (the batch is done)
   int seq, tpc;                 // tokens per CTA
   int64_t tok0, pos0;           // first token: row of the batch, position
   int ntok;                     // tokens of the pair
@@ -183,7 +192,9 @@ __device__ __forceinline__ bool block_clean(const Work& w, int kb) {
 // Tile `x` of the batch, counted from the last tile of the last sequence (the
 // longest rows of a sequence come first, which leaves short tiles for the end).
 // Whole-warp call.
-__device__ __forceinline__ bool find_work(const PairParams& p, int64_t x, int lane, Work& w) {
+__device__ __forceinline__ void find_work(const PairParams& p, int64_t x, int lane, Work& w) {
+  w.has = 0;
+  w.ntok = w.nb = w.nbw = 0;
   w.tpc = max(1, 64 / p.H);
   const int per = 2 * w.tpc;
   for (int b0 = p.n_seq - 1; b0 >= 0; b0 -= 32) {
@@ -211,7 +222,8 @@ __device__ __forceinline__ bool find_work(const PairParams& p, int64_t x, int la
     w.tok0 = (int64_t)p.cu_q[w.seq] + (int64_t)t * per;
     w.ntok = min(per, len - t * per);
     w.pos0 = p.q_pos[w.seq] + (int64_t)t * per;
-    if (w.tok0 < 0 || w.tok0 + w.ntok > p.n_tok) return false;
+    if (w.tok0 < 0 || w.tok0 + w.ntok > p.n_tok) return;
+    w.has = 1;
     const int64_t last = w.pos0 + w.ntok - 1;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -224,9 +236,8 @@ __device__ __forceinline__ bool find_work(const PairParams& p, int64_t x, int la
     w.wb0 = w.any_lo[0] / kBlock;
     w.nbw = w.any_hi[0] > w.any_lo[0] ? (int)((w.any_hi[0] + kBlock - 1) / kBlock - w.wb0) : 0;
     w.nb = w.nbw + (int)((w.any_hi[1] + kBlock - 1) / kBlock);
-    return true;
+    return;
   }
-  return false;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -240,37 +251,39 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
   uint8_t* sP = sQ + 8 * kSlab;                              // [4 slabs][64 rows][128 B]
   uint8_t* sRing = sP + 4 * kSlab;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sRing + kStages * kStage);
-  uint64_t* full = bars;                                     // [4] CTA 0: a stage's parts in both CTAs are there
-  uint64_t* empty = full + kStages;                          // [4] the MMAs that read a stage are done
+  // CTA 0: the parts of a K (V) stage in both CTAs are there.  Apart for K and V:
+  // a wait tells two neighbouring phases apart, no more, so a barrier that is
+  // waited on must not advance by uses that its waiter does not see.
+  uint64_t* full_k = bars;                                   // [4]
+  uint64_t* full_v = full_k + kStages;                       // [4]
+  uint64_t* empty = full_v + kStages;                        // [4] the MMAs that read a stage are done
   uint64_t* go = empty + kStages;                            // [4] the stage is the copying warps' to fill
   uint64_t* q_full = go + kStages;                           // CTA 0: the queries of both CTAs
-  uint64_t* s_full = q_full + 1;                             // [2]
+  uint64_t* q_free = q_full + 1;                             // the S products of an item are done
+  uint64_t* o_free = q_free + 1;                             // CTA 0: an item's output is out of TMEM in both CTAs
+  uint64_t* w_full = o_free + 1;                             // [4] an item is in s_work ...
+  uint64_t* w_free = w_full + kItems;                        // [4] ... and every warp has read it
+  uint64_t* s_full = w_free + kItems;                        // [2]
   uint64_t* s_free = s_full + 2;                             // [2] CTA 0: read by the softmax of both CTAs
   uint64_t* p_full = s_free + 2;                             // CTA 0: P and the rescaled O of both CTAs
   uint64_t* pv_done = p_full + 1;
   float* s_x = reinterpret_cast<float*>(pv_done + 1);        // [2][2][64] maxima / sums of the row halves
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_x + 256);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
-  __shared__ Work s_work;
-  __shared__ int s_has;
+  __shared__ Work s_work[kItems];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t cta = cta_rank();
-  if (warp == 0) {
-    Work w;
-    const bool has = find_work(p, blockIdx.x >> 1, lane, w);
-    if (lane == 0) { s_work = w; s_has = has; }
-  }
-  if (tid == 32) {
-    for (int i = 0; i < kStages; ++i) { mbar_init(&full[i], 2); mbar_init(&empty[i], 1); mbar_init(&go[i], 1); }
-    mbar_init(q_full, 2);
+  const int64_t n_clusters = gridDim.x >> 1, cluster = blockIdx.x >> 1;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) { mbar_init(&full_k[i], 2); mbar_init(&full_v[i], 2); mbar_init(&empty[i], 1); mbar_init(&go[i], 1); }
+    for (int i = 0; i < kItems; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_free[i], 11); }
+    mbar_init(q_full, 2); mbar_init(q_free, 1); mbar_init(o_free, 8);
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 8); }
     mbar_init(p_full, 8); mbar_init(pv_done, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
-  __syncthreads();
-  if (!s_has) return;                                        // the same in both CTAs
   if (warp == 5) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(s_tmem)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -281,117 +294,193 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   volatile int* abort_flag = s_abort;
-  const Work w = s_work;
-  const int nt = (w.nb + kTileBlocks - 1) / kTileBlocks;     // tiles
 
-  // Stages in the order of the MMAs: K(0) K(1) V(0) K(2) V(1) ...  K(i) is 4
-  // stages (dims 128 d ..), V(i) one for each of its blocks (the dims
-  // 256 j + 128 cta .. of j = 0, 1).  A stage has one arrival from each CTA.
-  auto blocks_of = [&](int i) { return min(kTileBlocks, w.nb - kTileBlocks * i); };
+  // Item k of this cluster, from the ring that warp 10 fills.  Whole-warp call; no
+  // item: the batch is done, or a wait expired.  The four warps of a role that
+  // shares a barrier (bar) get one answer.  The last reader of a role releases it.
+  auto next_item = [&](uint32_t k, Work& w, uint32_t bar, bool release) -> bool {
+    const uint32_t sl = k % kItems;
+    bool ok = wait_warp(&w_full[sl], (k / kItems) & 1, abort_flag);
+    if (bar != 0 && named_bar_or(bar, 128, !ok)) ok = false;
+    if (!ok) return false;
+    w = s_work[sl];
+    __syncwarp();
+    if (release && lane == 0) mbar_arrive(&w_free[sl]);
+    return w.has != 0;
+  };
+  auto tiles_of = [](const Work& w) { return (w.nb + kTileBlocks - 1) / kTileBlocks; };
+  // Stages in their order: K(0), K(1), then the stages of V(t) and K(t + 2) in turn
+  // for t = 0, 1, ...  K is 4 stages (dims 128 d ..), V one for each of the tile's
+  // blocks (the dims 256 j + 128 cta .. of j = 0, 1).  A stage has one arrival from
+  // each CTA.
+  auto blocks_of = [](const Work& w, int i) { return min(kTileBlocks, w.nb - kTileBlocks * i); };
 
-  if (warp == 4) {
-    // ============================ TMA producer
-    if (lane == 0) {
-      expect_leader(q_full, 8 * kSlab);
-      for (int s = 0; s < 8; ++s)
-        tma_load_pair(sQ + s * kSlab, &map_q, 64 * s, (int32_t)((w.tok0 + (int64_t)cta * w.tpc) * p.H), q_full);
+  // The tiles of all items in their order (items without rows have none).
+  struct Stream {
+    Work w;
+    uint32_t k = 0, items = 0;   // items read; items with tiles so far, the present one included
+    int i = 0, nt = 0;           // tile of the item
+    bool on = true;              // whether there is one
+  };
+  auto advance = [&](Stream& x, uint32_t bar, bool release) {
+    if (++x.i < x.nt || !x.on) return;
+    do {
+      x.on = next_item(x.k++, x.w, bar, release);
+      if (!x.on) return;
+      x.nt = tiles_of(x.w);
+    } while (x.nt == 0);
+    x.i = 0;
+    ++x.items;
+  };
+
+  if (warp == 7) {
+    // ============================ items
+    for (uint32_t k = 0;; ++k) {
+      const uint32_t sl = k % kItems;
+      Work w;
+      find_work(p, cluster + (int64_t)k * n_clusters, lane, w);
+      if (!wait_warp(&w_free[sl], ((k / kItems) & 1) ^ 1, abort_flag)) break;
+      if (lane == 0) {
+        s_work[sl] = w;
+        mbar_arrive(&w_full[sl]);
+      }
+      if (!w.has) break;
     }
+  } else if (warp == 4) {
+    // ============================ TMA producer
     // Lane 4 kb + j has part j of block kb of a tile: pages of less than 64 rows
-    // make several boxes of a block.  It looks its row of the page store up a tile
-    // ahead and issues the copies of its part itself.
+    // make several boxes of a block.  It looks its row of the page store up and
+    // issues the copies of its part itself.
     uint32_t st = 0;                                         // stages so far
     bool ok = true;
     const int kb = lane >> 2, j = lane & 3;
     struct Part { int32_t y; int s, rows; bool on; };        // first row, source, rows; whether there is one
-    auto part_of = [&](int i) {
+    auto part_of = [&](const Stream& x) {
       Part t{0, 0, kBlock, false};
-      if (i < nt && kb < blocks_of(i)) {
+      if (x.on && kb < blocks_of(x.w, x.i)) {
         int64_t row;
-        t.s = block_at(w, kTileBlocks * i + kb, row);
+        t.s = block_at(x.w, kTileBlocks * x.i + kb, row);
         const PageTable& pt = t.s ? p.pt[1] : p.pt[0];
         t.rows = min(kBlock, 1 << pt.ps_log2);
         t.on = j * t.rows < kBlock;
         if (t.on) {
-          const int64_t g = page_row(pt, w.seq, row + j * t.rows);
+          const int64_t g = page_row(pt, x.w.seq, row + j * t.rows);
           // A part without a page reads page 0.  It has no visible row, so its logits
           // are masked and its V is not loaded here; or the table is wrong.
-          if (g < 0 && block_clean(w, kTileBlocks * i + kb)) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
+          if (g < 0 && block_clean(x.w, kTileBlocks * x.i + kb)) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
           t.y = (int32_t)max((int64_t)0, g);
         }
       }
       return t;
     };
     auto wait_empty = [&](uint32_t sl) {                     // one answer for the warp
-      ok = __all_sync(0xffffffffu, wait(&empty[sl], ((st / kStages) & 1) ^ 1, abort_flag));
+      ok = wait_warp(&empty[sl], ((st / kStages) & 1) ^ 1, abort_flag);
       return ok;
     };
-    auto load_k = [&](int i, const Part& t) {
-      // blocks 2 cta, 2 cta + 1 of the tile; absent ones are not loaded (their logits are masked)
-      const int n = max(0, min(2, blocks_of(i) - 2 * (int)cta));
-      const bool mine = t.on && (kb >> 1) == (int)cta;
-      const CUtensorMap* map = t.s ? &map_ent : &map_raw;
-      for (int d = 0; d < kKStages; ++d, ++st) {
-        const uint32_t sl = st % kStages;
-        if (!wait_empty(sl)) break;
-        if (lane == 0) {
-          if (n) expect_leader(&full[sl], n * 2 * kSlab);
-          else arrive_leader(&full[sl]);
-        }
-        if (mine) {
-          uint8_t* dst = sRing + sl * kStage + (kb & 1) * kSlab + j * t.rows * 128;
-          tma_load_pair(dst, map, 128 * d, t.y, &full[sl]);
-          tma_load_pair(dst + 2 * kSlab, map, 128 * d + 64, t.y, &full[sl]);
-        }
+    auto load_q = [&](const Stream& x) {
+      ok = wait_warp(q_free, x.items & 1, abort_flag);
+      if (ok && lane == 0) {
+        expect_leader(q_full, 8 * kSlab);
+        for (int s = 0; s < 8; ++s)
+          tma_load_pair(sQ + s * kSlab, &map_q, 64 * s, (int32_t)((x.w.tok0 + (int64_t)cta * x.w.tpc) * p.H), q_full);
       }
+      __syncwarp();
     };
-    auto load_v = [&](int i, const Part& t) {
+    auto load_k = [&](const Stream& x, const Part& t, int d) {
+      // blocks 2 cta, 2 cta + 1 of the tile; absent ones are not loaded (their logits are masked)
+      const int n = max(0, min(2, blocks_of(x.w, x.i) - 2 * (int)cta));
       const CUtensorMap* map = t.s ? &map_ent : &map_raw;
-      const int nbk = blocks_of(i);
-      for (int v = 0; v < nbk && ok; ++v, ++st) {
-        const uint32_t sl = st % kStages;
-        if (!wait_empty(sl)) break;
-        if (!block_clean(w, kTileBlocks * i + v)) {          // the copying warps'
-          if (lane == 0) mbar_arrive(&go[sl]);
-          continue;
-        }
-        if (lane == 0) expect_leader(&full[sl], kStage);
+      const uint32_t sl = st % kStages;
+      if (!wait_empty(sl)) return;
+      if (lane == 0) {
+        if (n) expect_leader(&full_k[sl], n * 2 * kSlab);
+        else arrive_leader(&full_k[sl]);
+      }
+      if (t.on && (kb >> 1) == (int)cta) {
+        uint8_t* dst = sRing + sl * kStage + (kb & 1) * kSlab + j * t.rows * 128;
+        tma_load_pair(dst, map, 128 * d, t.y, &full_k[sl]);
+        tma_load_pair(dst + 2 * kSlab, map, 128 * d + 64, t.y, &full_k[sl]);
+      }
+      ++st;
+    };
+    auto load_v = [&](const Stream& x, const Part& t, int v) {
+      const CUtensorMap* map = t.s ? &map_ent : &map_raw;
+      const uint32_t sl = st % kStages;
+      if (!wait_empty(sl)) return;
+      if (!block_clean(x.w, kTileBlocks * x.i + v)) {        // the copying warps'
+        if (lane == 0) mbar_arrive(&go[sl]);
+      } else {
+        if (lane == 0) expect_leader(&full_v[sl], kStage);
         if (t.on && kb == v) {
           uint8_t* dst = sRing + sl * kStage + j * t.rows * 128;
 #pragma unroll
           for (int h = 0; h < 4; ++h)
-            tma_load_pair(dst + h * kSlab, map, 256 * (h >> 1) + 128 * (int)cta + 64 * (h & 1), t.y, &full[sl]);
+            tma_load_pair(dst + h * kSlab, map, 256 * (h >> 1) + 128 * (int)cta + 64 * (h & 1), t.y, &full_v[sl]);
         }
       }
+      ++st;
     };
-    Part cur = part_of(0), next = part_of(1);
-    if (nt > 0) load_k(0, cur);
-    for (int i = 0; i < nt && ok; ++i) {
-      const Part after = part_of(i + 2);
-      if (i + 1 < nt) load_k(i + 1, next);
-      if (ok) load_v(i, cur);
-      cur = next;
-      next = after;
+    Stream x0, x1, x2;                                       // tiles t, t + 1, t + 2
+    Part p0, p1, p2;
+    advance(x0, 0, true);
+    p0 = part_of(x0);
+    x1 = x0;
+    if (x0.on) load_q(x0);
+    for (int d = 0; d < kKStages && x0.on && ok; ++d) load_k(x0, p0, d);
+    advance(x1, 0, true);
+    p1 = part_of(x1);
+    x2 = x1;
+    if (x1.on && x1.i == 0 && ok) load_q(x1);
+    for (int d = 0; d < kKStages && x1.on && ok; ++d) load_k(x1, p1, d);
+    while (x0.on && ok) {
+      advance(x2, 0, true);
+      p2 = part_of(x2);
+      // the next item's queries, once S(t + 1) is done with the present ones
+      const bool q = x2.on && x2.i == 0;
+      for (int d = 0; d < kTileBlocks && ok; ++d) {
+        if (d < blocks_of(x0.w, x0.i)) load_v(x0, p0, d);
+        if (d == 0 && q && ok) load_q(x2);
+        if (x2.on && ok) load_k(x2, p2, d);
+      }
+      x0 = x1; p0 = p1;
+      x1 = x2; p1 = p2;
     }
-  } else if (warp >= 6) {
+  } else if (warp >= 8) {
     // ============================ copies of V blocks that not every token sees
-    const int lt = tid - 192;                                // 0 .. 127
+    const int lt = tid - 256;                                // 0 .. 127
     // They see few of the stages, so the phase of `empty` tells them nothing (a
     // parity is ambiguous two phases on): the producer, which sees all of them,
     // hands a stage over through its `go`, once for each use.
     uint32_t st = 0, uses = 0;                               // uses: bit sl, parity of the next use
     bool ok = true;
-    if (nt > 0) st += kKStages;
-    for (int i = 0; i < nt && ok; ++i) {
-      if (i + 1 < nt) st += kKStages;
-      const int nbk = blocks_of(i);
-      for (int kb = 0; kb < nbk && ok; ++kb, ++st) {
+    Stream x;                                                // tile t + 2
+    Work w0, w1;                                             // items of tiles t, t + 1
+    int i0, i1, nb0, nb1;                                    // their tiles of the item, and their blocks (0: no tile)
+    auto take = [&](Work& w, int& i, int& nb) {
+      w = x.w;
+      i = x.i;
+      nb = x.on ? blocks_of(x.w, x.i) : 0;
+    };
+    advance(x, 2, true);
+    take(w0, i0, nb0);
+    if (x.on) st += kKStages;
+    advance(x, 2, true);
+    take(w1, i1, nb1);
+    if (x.on) st += kKStages;
+    while (nb0 > 0 && ok) {
+      advance(x, 2, true);
+      const Work& w = w0;
+      const uint32_t step = x.on ? 2 : 1;                    // a K stage follows each V stage
+      for (int kb = 0; kb < nb0 && ok; ++kb) {
+        const uint32_t sv = st + step * kb;
+        const int i = i0;
         if (block_clean(w, kTileBlocks * i + kb)) continue;
         int64_t row0;
         const int s = block_at(w, kTileBlocks * i + kb, row0);
         const PageTable& pt = s ? p.pt[1] : p.pt[0];
         const __nv_bfloat16* store = static_cast<const __nv_bfloat16*>(s ? p.rows[1] : p.rows[0]);
         const int64_t lo = s ? w.any_lo[1] : w.any_lo[0], hi = s ? w.any_hi[1] : w.any_hi[0];
-        const uint32_t sl = st % kStages;
+        const uint32_t sl = sv % kStages;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           // 64 rows x 128 dims: 16 pieces of 16 bytes a row, 16 lanes on a row
@@ -408,7 +497,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
             }
           }
           if (j == 0) {
-            ok = wait(&go[sl], (uses >> sl) & 1, abort_flag);
+            ok = wait_warp(&go[sl], (uses >> sl) & 1, abort_flag);
             uses ^= 1u << sl;
             if (named_bar_or(2, 128, !ok)) ok = false;       // one answer for the four warps
             if (!ok) break;
@@ -423,59 +512,103 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
         if (!ok) break;
         fence_proxy_async_smem();
         named_bar_sync(2, 128);
-        if (lt == 0) arrive_leader(&full[sl]);
+        if (lt == 0) arrive_leader(&full_v[sl]);
       }
+      st += nb0 + (x.on ? kKStages : 0);
+      w0 = w1;
+      i0 = i1;
+      nb0 = nb1;
+      take(w1, i1, nb1);
     }
-  } else if (warp == 5) {
-    if (cta == 0 && lane == 0) {
-      // ============================ MMA issuer
-      const uint32_t idesc_s = make_idesc(128, 256, 1, 1, 0, 0);
-      const uint32_t idesc_o = make_idesc(128, 256, 1, 1, 0, 1);
+  } else if (warp == 5 || warp == 6) {
+    // ============================ MMA issuers: lane 0 of CTA 0, warp 5 of S, warp 6 of PV
+    const bool issue = cta == 0 && lane == 0;
+    uint32_t st = 0, t = 0;                                  // stages and tiles so far
+    bool ok = true;
+    uint32_t uses = 0;                                       // bit sl: parity of this issuer's next use of slot sl
+    auto ready = [&](uint64_t* full, uint32_t sl) {
+      ok = ok && wait(&full[sl], (uses >> sl) & 1, abort_flag);
+      uses ^= 1u << sl;
+      tc_fence_after();
+      return ok;
+    };
+    Stream x;                                                // tile t + 2
+    auto blocks = [&]() { return x.on ? blocks_of(x.w, x.i) : 0; };
+    if (warp == 5) {
+      const uint32_t idesc = make_idesc(128, 256, 1, 1, 0, 0);
       const uint64_t dQ = smem_desc(smem_u32(sQ), 16, 1024, SWZ_128B);
-      const uint64_t dP = smem_desc(smem_u32(sP), 16, 1024, SWZ_128B);
       const uint64_t dK = smem_desc(smem_u32(sRing), 16, 1024, SWZ_128B);
-      const uint64_t dV = smem_desc(smem_u32(sRing), kSlab, 1024, SWZ_128B);
-      uint32_t st = 0;
-      bool ok = wait(q_full, 0, abort_flag);
-      auto stage = [&]() {
-        const uint32_t sl = st % kStages, ph = (st / kStages) & 1;
-        ok = ok && wait(&full[sl], ph, abort_flag);
-        tc_fence_after();
-        ++st;
-        return sl;
-      };
-      auto do_s = [&](int i) {
-        ok = ok && wait(&s_free[i & 1], ((i >> 1) & 1) ^ 1, abort_flag);
+      // S of the stream's tile, number n; nv V stages alternate with its own
+      auto do_s = [&](uint32_t n, int nv) {
+        if (x.i == 0) ok = ok && wait(q_full, (x.items & 1) ^ 1, abort_flag);
+        ok = ok && wait(&s_free[n & 1], ((n >> 1) & 1) ^ 1, abort_flag);
         for (int d = 0; d < kKStages && ok; ++d) {
-          const uint32_t sl = stage();
-          if (!ok) break;
+          const uint32_t sl = (st + d + min(d + 1, nv)) % kStages;
+          if (!ready(full_k, sl)) break;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_pair(tmem + kSCol + 128 * (i & 1), dQ + (((2 * d + (k >> 2)) * kSlab + (k & 3) * 32) >> 4),
-                     dK + ((sl * kStage + (k >> 2) * 2 * kSlab + (k & 3) * 32) >> 4), idesc_s, (d | k) != 0);
+          for (int m = 0; m < 8; ++m)
+            mma_pair(tmem + kSCol + 128 * (n & 1), dQ + (((2 * d + (m >> 2)) * kSlab + (m & 3) * 32) >> 4),
+                     dK + ((sl * kStage + (m >> 2) * 2 * kSlab + (m & 3) * 32) >> 4), idesc, (d | m) != 0);
           commit_pair(&empty[sl]);
         }
-        if (ok) commit_pair(&s_full[i & 1]);
-      };
-      auto do_pv = [&](int i) {
-        ok = ok && wait(p_full, i & 1, abort_flag);
-        const int nbk = blocks_of(i);
-        for (int kb = 0; kb < nbk && ok; ++kb) {
-          const uint32_t sl = stage();
-          if (!ok) break;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_pair(tmem + 128 * (k >> 2), dP + ((kb * kSlab + (k & 3) * 32) >> 4),
-                     dV + ((sl * kStage + (k >> 2) * 2 * kSlab + (k & 3) * 2048) >> 4), idesc_o,
-                     (i | kb | (k & 3)) != 0);
-          commit_pair(&empty[sl]);
+        if (ok) {
+          commit_pair(&s_full[n & 1]);
+          if (x.i == x.nt - 1) commit_pair(q_free);
         }
-        if (ok) commit_pair(pv_done);
       };
-      if (nt > 0) do_s(0);
-      for (int i = 0; i < nt && ok; ++i) {
-        if (i + 1 < nt) do_s(i + 1);
-        if (ok) do_pv(i);
+      advance(x, 0, true);
+      int nb0 = blocks();
+      if (issue && x.on) do_s(0, 0);
+      if (x.on) st += kKStages;
+      __syncwarp();
+      advance(x, 0, true);
+      int nb1 = blocks();
+      if (issue && x.on) do_s(1, 0);
+      if (x.on) st += kKStages;
+      __syncwarp();
+      for (; nb0 > 0; ++t) {
+        advance(x, 0, true);
+        if (issue && x.on && ok) do_s(t + 2, nb0);
+        st += nb0 + (x.on ? kKStages : 0);
+        nb0 = nb1;
+        nb1 = blocks();
+        __syncwarp();
+      }
+    } else {
+      const uint32_t idesc = make_idesc(128, 256, 1, 1, 0, 1);
+      const uint64_t dP = smem_desc(smem_u32(sP), 16, 1024, SWZ_128B);
+      const uint64_t dV = smem_desc(smem_u32(sRing), kSlab, 1024, SWZ_128B);
+      struct Tile { int i, items, nb; };
+      auto take = [&]() { return Tile{x.i, (int)x.items, blocks()}; };
+      advance(x, 0, true);
+      Tile t0 = take();
+      if (x.on) st += kKStages;
+      advance(x, 0, true);
+      Tile t1 = take();
+      if (x.on) st += kKStages;
+      for (; t0.nb > 0; ++t) {
+        advance(x, 0, true);
+        const uint32_t step = x.on ? 2 : 1;                  // a K stage follows each V stage
+        if (issue && ok) {
+          // O is overwritten at an item's first tile: the item before must be out of it
+          if (t0.i == 0) ok = ok && wait(o_free, t0.items & 1, abort_flag);
+          ok = ok && wait(p_full, t & 1, abort_flag);
+          for (int kb = 0; kb < t0.nb && ok; ++kb) {
+            const uint32_t sl = (st + step * kb) % kStages;
+            if (!ready(full_v, sl)) break;
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+              mma_pair(tmem + 128 * (m >> 2), dP + ((kb * kSlab + (m & 3) * 32) >> 4),
+                       dV + ((sl * kStage + (m >> 2) * 2 * kSlab + (m & 3) * 2048) >> 4), idesc,
+                       (t0.i | kb | (m & 3)) != 0);
+            commit_pair(&empty[sl]);
+          }
+          if (ok) commit_pair(pv_done);
+        }
+        st += t0.nb + (x.on ? kKStages : 0);
+        t0 = t1;
+        t1 = take();
+        __syncwarp();
       }
     }
     __syncwarp();
@@ -483,161 +616,192 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
     // ============================ softmax and epilogue: lane tid of TMEM
     const int r = tid & 63, half = tid >> 6;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const int tk = (int)cta * w.tpc + r / p.H;               // this row's token of the pair
-    const bool valid = r < w.tpc * p.H && tk < w.ntok && w.pos0 + tk >= 0;
-    const int64_t pos = valid ? w.pos0 + tk : -1;
-    int64_t lo[2], hi[2];
-    seen(p, 0, pos, lo[0], hi[0]);
-    seen(p, 1, pos, lo[1], hi[1]);
-    float m = -CUDART_INF_F, l = 0.f;
+    uint32_t g = 0, bc = 0;                                  // tiles and exchanges of the items before
     bool ok = true;
-    // After a wait that expired the warps only keep their barriers, so that none
-    // waits for another for ever.
-    for (int i = 0; i < nt; ++i) {
-      ok = __all_sync(0xffffffffu, ok && wait(&s_full[i & 1], (i >> 1) & 1, abort_flag));
-      tc_fence_after();
-      const uint32_t ts = tmem + lane_base + kSCol + 128 * (i & 1);
-      // which of this thread's 128 columns (blocks 2 half, 2 half + 1) the row's token sees
-      uint64_t see[2];
+    Work w;
+    for (uint32_t k = 0; next_item(k, w, 1, true); ++k) {
+      const int nt = tiles_of(w);
+      const int tk = (int)cta * w.tpc + r / p.H;               // this row's token of the pair
+      const bool valid = r < w.tpc * p.H && tk < w.ntok && w.pos0 + tk >= 0;
+      const int64_t pos = valid ? w.pos0 + tk : -1;
+      int64_t lo[2], hi[2];
+      seen(p, 0, pos, lo[0], hi[0]);
+      seen(p, 1, pos, lo[1], hi[1]);
+      float m = -CUDART_INF_F, l = 0.f;
+      // After a wait that expired the warps only keep their barriers, so that none
+      // waits for another for ever.
+      for (int i = 0; i < nt; ++i) {
+        const uint32_t t = g + i;
+        ok = ok && wait_warp(&s_full[t & 1], (t >> 1) & 1, abort_flag);
+        tc_fence_after();
+        const uint32_t ts = tmem + lane_base + kSCol + 128 * (t & 1);
+        // which of this thread's 128 columns (blocks 2 half, 2 half + 1) the row's token sees
+        uint64_t see[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int kb = kTileBlocks * i + 2 * half + h;
-        see[h] = 0;
-        if (kb < w.nb) {
-          int64_t row;
-          const int s = block_at(w, kb, row);
-          const int64_t a = lo[s] - row, e = hi[s] - row;    // visible: [a, e) of the block
-          const uint64_t below = e >= 64 ? ~0ull : e <= 0 ? 0ull : (1ull << e) - 1;
-          const uint64_t from = a <= 0 ? ~0ull : a >= 64 ? 0ull : ~((1ull << a) - 1);
-          see[h] = below & from;
+        for (int h = 0; h < 2; ++h) {
+          const int kb = kTileBlocks * i + 2 * half + h;
+          see[h] = 0;
+          if (kb < w.nb) {
+            int64_t row;
+            const int s = block_at(w, kb, row);
+            const int64_t a = (s ? lo[1] : lo[0]) - row, e = (s ? hi[1] : hi[0]) - row;   // visible: [a, e) of the block
+            const uint64_t below = e >= 64 ? ~0ull : e <= 0 ? 0ull : (1ull << e) - 1;
+            const uint64_t from = a <= 0 ? ~0ull : a >= 64 ? 0ull : ~((1ull << a) - 1);
+            see[h] = below & from;
+          }
         }
-      }
-      // pass 1: the maximum of the visible logits
-      float mx = -CUDART_INF_F;
+        // whether every row of the warp sees all 64 columns of a block
+        const bool whole[2] = {__all_sync(0xffffffffu, see[0] == ~0ull) != 0, __all_sync(0xffffffffu, see[1] == ~0ull) != 0};
+        // pass 1: the maximum of the visible logits
+        float mx = -CUDART_INF_F;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (!ok) break;
+          float x[32];
+          tmem_ld32(ts + 32 * c, x);
+          tmem_wait_ld();
+          if (!whole[c >> 1]) {
+            const uint32_t bits = (uint32_t)(see[c >> 1] >> (32 * (c & 1)));
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = (bits >> k) & 1u ? x[k] : -CUDART_INF_F;
+          }
+          float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int k = 4; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], x[k]);
+          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+        }
+        float* sx = s_x + (bc++ & 1) * 128;
+        sx[half * 64 + r] = mx;
+        if (named_bar_or(1, 128, !ok)) ok = false;
+        if (!ok) continue;
+        mx = fmaxf(sx[r], sx[64 + r]) * p.scale_log2;
+        // The maximum moves only when it grows by more than 2^kTau.
+        float alpha = 1.f;
+        if (mx > m + kTau) {
+          alpha = exp2f(m - mx);                               // 0 the first time
+          m = mx;
+        }
+        l *= alpha;
+      const float ref = m == -CUDART_INF_F ? 0.f : m;
+      // pass 2: probabilities, as bf16 pairs in registers
+      uint32_t pk[64];
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        if (!ok) break;
         float x[32];
         tmem_ld32(ts + 32 * c, x);
         tmem_wait_ld();
-        const uint32_t bits = (uint32_t)(see[c >> 1] >> (32 * (c & 1)));
-        if (bits == 0xffffffffu) {
+        if (!whole[c >> 1]) {
+          // a visible logit of -inf is a non-finite row's, whose V may read as zeros
+          const uint32_t bits = (uint32_t)(see[c >> 1] >> (32 * (c & 1)));
 #pragma unroll
-          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, x[k]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, (bits >> k) & 1u ? x[k] : -CUDART_INF_F);
+          for (int q = 0; q < 32; ++q)
+            x[q] = !((bits >> q) & 1u) ? -CUDART_INF_F : x[q] == -CUDART_INF_F ? CUDART_NAN_F : x[q];
         }
+#pragma unroll
+        for (int q = 0; q < 32; ++q) x[q] = exp2_fast(fmaf(x[q], p.scale_log2, -ref));
+#pragma unroll
+        for (int q = 0; q < 32; ++q) l4[q & 3] += x[q];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) pk[16 * c + q] = pack2(x[2 * q], x[2 * q + 1]);
       }
-      float* sx = s_x + (i & 1) * 128;
-      sx[half * 64 + r] = mx;
-      if (named_bar_or(1, 128, !ok)) ok = false;
-      if (!ok) continue;
-      mx = fmaxf(sx[r], sx[64 + r]) * p.scale_log2;
-      // The maximum moves only when it grows by more than 2^kTau.
-      float alpha = 1.f;
-      if (mx > m + kTau) {
-        alpha = exp2f(m - mx);                               // 0 the first time
-        m = mx;
-      }
-      l *= alpha;
-      const float ref = m == -CUDART_INF_F ? 0.f : m;
-      // P and O are free once PV(i - 1) is done
+      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader(&s_free[t & 1]);
+      // P and O are free once PV(t - 1) is done (of an earlier item: its epilogue waited)
       if (i > 0) {
-        ok = __all_sync(0xffffffffu, wait(pv_done, (i - 1) & 1, abort_flag));
+        ok = wait_warp(pv_done, (t - 1) & 1, abort_flag);
         if (!ok) continue;
         tc_fence_after();
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            float o[32];
-            tmem_ld32(tmem + lane_base + 32 * c, o);
+          for (int c = 0; c < 16; ++c) {
+            float o[16];
+            tmem_ld16(tmem + lane_base + 16 * c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= alpha;
-            tmem_st32(tmem + lane_base + 32 * c, o);
+            for (int q = 0; q < 16; ++q) o[q] *= alpha;
+            tmem_st16(tmem + lane_base + 16 * c, o);
           }
           tmem_wait_st();
+          tc_fence_before();
         }
       }
-      // pass 2: probabilities
       const uint32_t pb = smem_u32(sP) + (2 * half) * kSlab;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float x[32];
-        tmem_ld32(ts + 32 * c, x);
-        tmem_wait_ld();
-        const uint32_t bits = (uint32_t)(see[c >> 1] >> (32 * (c & 1)));
-        if (bits == 0xffffffffu) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = exp2_fast(fmaf(x[k], p.scale_log2, -ref));
-        } else {
-          // a visible logit of -inf is a non-finite row's, whose V may read as zeros
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            x[k] = !((bits >> k) & 1u) ? 0.f : x[k] == -CUDART_INF_F ? CUDART_NAN_F : exp2_fast(fmaf(x[k], p.scale_log2, -ref));
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) l += x[k];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          st_shared16(pb + (c >> 1) * kSlab + swz128(r, 4 * (c & 1) + q),
-                      make_uint4(pack2(x[8 * q], x[8 * q + 1]), pack2(x[8 * q + 2], x[8 * q + 3]),
-                                 pack2(x[8 * q + 4], x[8 * q + 5]), pack2(x[8 * q + 6], x[8 * q + 7])));
-      }
-      tc_fence_before();
+      for (int q = 0; q < 16; ++q)
+        st_shared16(pb + (q >> 3) * kSlab + swz128(r, q & 7), make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        arrive_leader(&s_free[i & 1]);
-        arrive_leader(p_full);
-      }
+      if (lane == 0) arrive_leader(p_full);
     }
     // ---------------- epilogue
-    {
-      float* sx = s_x + (nt & 1) * 128;
-      sx[half * 64 + r] = l;
-      named_bar_sync(1, 128);
-      l = sx[r] + sx[64 + r];
-      float coef = 0.f;
-      if (valid) {
-        const float sk = p.sink ? p.sink[r % p.H] * 1.4426950408889634f : -CUDART_INF_F;
-        if (l != 0.f || sk != -CUDART_INF_F) {               // a NaN sum passes
-          const float top = fmaxf(l != 0.f ? m : -CUDART_INF_F, sk);
-          const float e = l != 0.f ? exp2f(m - top) : 0.f;
-          coef = l != 0.f ? e / (e * l + exp2f(sk - top)) : 0.f;
-        }
-      }
-      if (nt > 0) ok = __all_sync(0xffffffffu, ok && wait(pv_done, (nt - 1) & 1, abort_flag));
-      if (ok) {
-        tc_fence_after();
-        const int64_t orow = ((w.tok0 + tk) * p.H + r % p.H) * kD;
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          float o[32];
-          if (nt > 0) {
-            tmem_ld32(tmem + lane_base + 32 * c, o);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0.f;
+      {
+        float* sx = s_x + (bc++ & 1) * 128;
+        sx[half * 64 + r] = l;
+        named_bar_sync(1, 128);
+        l = sx[r] + sx[64 + r];
+        float coef = 0.f;
+        if (valid) {
+          const float sk = p.sink ? p.sink[r % p.H] * 1.4426950408889634f : -CUDART_INF_F;
+          if (l != 0.f || sk != -CUDART_INF_F) {               // a NaN sum passes
+            const float top = fmaxf(l != 0.f ? m : -CUDART_INF_F, sk);
+            const float e = l != 0.f ? exp2f(m - top) : 0.f;
+            coef = l != 0.f ? e / (e * l + exp2f(sk - top)) : 0.f;
           }
-          if (valid) {
+        }
+        g += nt;
+        if (nt > 0) ok = ok && wait_warp(pv_done, (g - 1) & 1, abort_flag);
+        tc_fence_after();
+        // Rows [first, rows) of this CTA are tokens' results.
+        const int64_t orow = (w.tok0 + (int64_t)cta * w.tpc) * p.H;
+        const int rows = max(0, min(w.tpc, w.ntok - (int)cta * w.tpc)) * p.H;
+        const int first = (int)min((int64_t)rows, max((int64_t)0, -(w.pos0 + (int64_t)cta * w.tpc)) * p.H);
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+          // columns 128 j + 32 c of O: dims 256 j + 128 half + 32 c.  A row of bf16
+          // goes through P's shared memory (P is done with), so that a warp writes 512
+          // bytes of one row at a time: rows written by their own threads took 4,000
+          // cycles an item more.
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            if (nt > 0 && ok) {
+              __syncwarp();
+              tmem_ld32(tmem + lane_base + 128 * j + 32 * c, o);
+              tmem_wait_ld();
+            } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = coef == 0.f ? 0.f : o[k] * coef;
-            // columns 128 j + 32 c' of O: dims 256 j + 128 half + 32 c'
-            const int d = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+              for (int q = 0; q < 32; ++q) o[q] = 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = coef == 0.f ? 0.f : o[q] * coef;
             if (p.out_bf16) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow + d);
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                dst[q] = make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
-                                    pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7]));
-            } else {
-              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + d);
+                st_shared16(smem_u32(sP) + (2 * half + (c >> 1)) * kSlab + swz128(r, 4 * (c & 1) + q),
+                            make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
+                                       pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7])));
+            } else if (valid && ok) {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (orow + r) * kD + 256 * j + 128 * half + 32 * c);
 #pragma unroll
               for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
             }
+          }
+          if (j == 1 && nt > 0) {                            // the next item may overwrite O
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_leader(o_free);
+          }
+          if (p.out_bf16) {
+            named_bar_sync(1, 128);
+            if (ok)
+              for (int rr = first + warp; rr < rows; rr += 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(sP + (lane >> 3) * kSlab + swz128(rr, lane & 7));
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (orow + rr) * kD + 256 * j + 8 * lane) = v;
+              }
+            if (j == 0) named_bar_sync(1, 128);
           }
         }
       }
@@ -673,14 +837,16 @@ csa_status_t launch_paged_pair(PairParams& p, cudaStream_t st) {
                    std::min(ps, kBlock), CU_TENSOR_MAP_SWIZZLE_128B))
       return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (pages) failed");
   }
-  const size_t smem = 1024 + 12 * kSlab + kStages * kStage + (3 * kStages + 7) * 8 + 256 * 4 + 16;
+  const size_t smem = 1024 + 12 * kSlab + kStages * kStage + (4 * kStages + 9 + 2 * kItems) * 8 + 256 * 4 + 16;
   cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
   // Every sequence's last tile may be partly filled: an upper bound of the tiles
   const int per = 2 * std::max(1, 64 / p.H);
   const int64_t tiles = std::min(p.n_tok, p.n_tok / per + p.n_seq);
   if (tiles > 0x3fffffff) return fail(CSA_ERR_UNSUPPORTED, "csa_paged_attention: too many tokens");
-  e = launch_pdl(pair_kernel, dim3((unsigned)(2 * tiles)), dim3(kThreads), smem, st, p, maps[0], maps[1], maps[2]);
+  // one cluster for every two SMs (one CTA fits an SM)
+  const int64_t clusters = std::min<int64_t>(tiles, num_sms() / 2);
+  e = launch_pdl(pair_kernel, dim3((unsigned)(2 * clusters)), dim3(kThreads), smem, st, p, maps[0], maps[1], maps[2]);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: launch failed: %s", cudaGetErrorString(e));
   return check_launch("csa_paged_attention");
 }

@@ -134,7 +134,7 @@ def _attn(L, **kw):
 
 @pytest.mark.parametrize("kw,text", [
     (dict(H=0), b"H must"), (dict(H=65), b"H must"), (dict(D=256), b"D must"), (dict(tp=None, kp=None), b"required"),
-    (dict(W=-1), b"W must"), (dict(odt=2), b"out_dtype"), (dict(q=ctypes.c_void_p(8)), b"aligned"), (dict(out=None), b"non-null"),
+    (dict(W=-1), b"W must"), (dict(sc=0.0), b"scale"), (dict(sc=-1.0), b"scale"), (dict(sc=math.nan), b"scale"), (dict(odt=2), b"out_dtype"), (dict(q=ctypes.c_void_p(8)), b"aligned"), (dict(out=None), b"non-null"),
     (dict(cu=None), b"cu_q"), (dict(tt=None), b"table"), (dict(tps=3), b"power of two"), (dict(kps=0), b"power of two"),
     (dict(kt=None), b"table"), (dict(kdt=0), b"kv_dtype"), (dict(kdt=2), b"kv_rope"), (dict(m=0), b"m must"),
     (dict(tmp=0), b"positive"), (dict(kn=0), b"positive"),
