@@ -16,13 +16,12 @@
 // [0, N/2) in lanes 0-63 and [N/2, N) in lanes 64-127: O takes 256 columns, two
 // S buffers 128 each, all 512.
 //
-// Operands stream through a ring of four 32 KB stages of 8 MMAs, K as 128 rows x
-// 128 dims, V as 64 rows x 256 dims.  A thread that issues MMAs loses about 270
-// cycles at every wait (its polls queue behind its MMAs, and the tensor pipe runs
-// dry meanwhile), so S and PV have an issuer each, on different schedulers, and
-// the stages of PV(t) and S(t + 2) alternate in the ring: each issuer's waits are
-// covered by the other's MMAs.  The softmax of tile t + 1 runs under both, keeps
-// its probabilities in registers, and writes them as soon as PV(t) has read P.
+// K and V stream through a ring of two 32 KB stages each (8 MMAs a stage): K as
+// 128 rows x 128 dims, V as 64 rows x 256 dims.  Each has a producer and an
+// issuer of its own (one thread cannot issue the copies of both, at about 100
+// cycles a copy).  PV(t) runs next to S(t + 2), and
+// the softmax of tile t + 1 under both: it holds its probabilities in registers
+// until PV(t) is done with P.
 //
 // Clusters are persistent and take every n-th pair of token groups (an item).
 // Tiles follow one another over the items, and one warp looks the items up ahead
@@ -61,11 +60,13 @@ namespace {
 constexpr int kD = 512;
 constexpr int kBlock = 64;                 // rows of a block: one page box, one slab of P
 constexpr int kTileBlocks = 4;             // 256 rows a tile
-constexpr int kStages = 4;
+constexpr int kStages = 2;                 // of each ring
 constexpr uint32_t kStage = 32768;         // K: [2 x 64 dims][128 rows], V: [4 x 64 dims][64 rows]
 constexpr int kKStages = 4;                // stages of a tile's K; its V has one for each block
 constexpr uint32_t kSlab = 8192;           // 64 rows x 128 bytes
-constexpr int kThreads = 384;              // warps 0-3 softmax, 4 TMA, 5 S and 6 PV (CTA 0), 7 items, 8-11 copies of V
+// warps 0-3 softmax and output, 4 loads Q and K, 7 loads V, 5 issues S and 6 PV
+// (in CTA 0), 8 and 9 copy V blocks, 10 looks up items
+constexpr int kThreads = 352;
 constexpr float kTau = 8.0f;               // lazy-rescale threshold (log2 units)
 constexpr uint32_t kSCol = 256;            // S buffers behind the 256 columns of O
 constexpr int kItems = 4;                  // items that are looked up ahead
@@ -124,14 +125,28 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, wait(bar, parity, abort_flag));
 }
+__device__ __forceinline__ void tma_load_pair_4d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                                int32_t u, uint64_t* bar) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %6, 0;\n\t"
+               "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+               " [%0], [%1, {%2, %3, %4, %5}], [a];\n\t}"
+               :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u),
+                  "r"(smem_u32(bar)) : "memory");
+}
+// MMAs and their commits are issued by whole warps in convergent code, with the
+// instruction itself predicated on one elected lane: descriptors then stay in
+// uniform registers, and a stage of 8 MMAs with its wait and its commit issues at
+// the tensor pipe's rate (64.9 cycles an MMA; from a branch that one lane takes,
+// 84 in a bare loop and 97 to 130 in this kernel).
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+               "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-// Arrive on *bar in both CTAs when every MMA issued by this thread so far is done.
+// Arrive on *bar in both CTAs when every MMA issued by the elected lane so far is done.
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+               "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
                :: "r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
@@ -153,41 +168,66 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   return lo | hi;
 }
 
-// The rows of a tile of tokens: blocks of 64 rows, raw rows first, then entries.
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+
+// An item: up to 2 tpc neighbouring tokens of a sequence, and the blocks of 64
+// rows that they see, raw rows first, then entries.
 struct Work {
   int has;                      // 0: no item (the batch is done)
   int seq, tpc;                 // tokens per CTA
   int64_t tok0, pos0;           // first token: row of the batch, position
   int ntok;                     // tokens of the pair
-  int64_t wb0;                  // first block of raw rows
+  int wb0;                      // first block of raw rows
   int nbw, nb;                  // blocks of raw rows, all blocks
-  int64_t any_lo[2], any_hi[2]; // rows of each source that some token sees ...
-  int64_t all_lo[2], all_hi[2]; // ... and that every token sees
+  int any_lo[2], any_hi[2];     // rows of each source that some token sees ...
+  int all_lo[2], all_hi[2];     // ... and that every token sees
 };
 
-// Rows [lo, hi) of source s (0 raw, 1 entries) that a query at position pos sees.
-__device__ __forceinline__ void seen(const PairParams& p, int s, int64_t pos, int64_t& lo, int64_t& hi) {
+// Rows [lo, hi) of source s (0 raw, 1 entries) that a query at position pos sees;
+// a table names fewer than 2^31 rows.
+__device__ __forceinline__ void seen(const PairParams& p, int s, int64_t pos, int& lo, int& hi) {
   lo = hi = 0;
   if (p.rows[s] == nullptr || pos < 0) return;
   if (s == 0) {
-    hi = min(p.cap[0], pos + 1);
-    lo = p.W == 0 ? 0 : min(hi, max((int64_t)0, pos - p.W + 1));
+    hi = (int)min(p.cap[0], pos + 1);
+    lo = p.W == 0 ? 0 : (int)min((int64_t)hi, max((int64_t)0, pos - p.W + 1));
   } else {
-    hi = min(p.cap[1], (pos + 1) / p.m);
+    hi = (int)min(p.cap[1], (pos + 1) / p.m);
   }
 }
 // Source and first row of block kb.
-__device__ __forceinline__ int block_at(const Work& w, int kb, int64_t& row) {
+__device__ __forceinline__ int block_at(const Work& w, int kb, int& row) {
   const int s = kb < w.nbw ? 0 : 1;
-  row = (s == 0 ? w.wb0 + kb : (int64_t)(kb - w.nbw)) * kBlock;
+  row = (s == 0 ? w.wb0 + kb : kb - w.nbw) * kBlock;
   return s;
 }
 // Whether every token of the pair sees every row of block kb.
 __device__ __forceinline__ bool block_clean(const Work& w, int kb) {
-  int64_t row;
+  int row;
   const int s = block_at(w, kb, row);
   return row >= (s ? w.all_lo[1] : w.all_lo[0]) && row + kBlock <= (s ? w.all_hi[1] : w.all_hi[0]);
 }
+
+// Tensor maps: the queries as [rows, 512], boxes of 64 x 64; each page store for
+// K as [rows, 512], boxes of (at most 64 rows of a page) x 64, and for V as
+// [2 of 256 dims][4 of 64][rows][64], boxes of 2 x 2 x rows x 64: a CTA's V block
+// is one copy.
+struct PairMaps {
+  CUtensorMap q, k[2], v[2];
+};
 
 // Tile `x` of the batch, counted from the last tile of the last sequence (the
 // longest rows of a sequence come first, which leaves short tiles for the end).
@@ -227,37 +267,36 @@ __device__ __forceinline__ void find_work(const PairParams& p, int64_t x, int la
     const int64_t last = w.pos0 + w.ntok - 1;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      int64_t z;
+      int z;
       seen(p, s, max(w.pos0, (int64_t)0), w.any_lo[s], z);
       seen(p, s, last, z, w.any_hi[s]);
       seen(p, s, last, w.all_lo[s], z);
       seen(p, s, w.pos0, z, w.all_hi[s]);
     }
     w.wb0 = w.any_lo[0] / kBlock;
-    w.nbw = w.any_hi[0] > w.any_lo[0] ? (int)((w.any_hi[0] + kBlock - 1) / kBlock - w.wb0) : 0;
-    w.nb = w.nbw + (int)((w.any_hi[1] + kBlock - 1) / kBlock);
+    w.nbw = w.any_hi[0] > w.any_lo[0] ? (w.any_hi[0] + kBlock - 1) / kBlock - w.wb0 : 0;
+    w.nb = w.nbw + (w.any_hi[1] + kBlock - 1) / kBlock;
     return;
   }
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap map_q,
-            const __grid_constant__ CUtensorMap map_raw, const __grid_constant__ CUtensorMap map_ent) {
+pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMaps maps) {
   extern __shared__ uint8_t smem_raw[];
   pdl_wait();
   pdl_trigger();
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;                                        // [8 slabs][64 rows][128 B]
   uint8_t* sP = sQ + 8 * kSlab;                              // [4 slabs][64 rows][128 B]
-  uint8_t* sRing = sP + 4 * kSlab;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sRing + kStages * kStage);
-  // CTA 0: the parts of a K (V) stage in both CTAs are there.  Apart for K and V:
-  // a wait tells two neighbouring phases apart, no more, so a barrier that is
-  // waited on must not advance by uses that its waiter does not see.
-  uint64_t* full_k = bars;                                   // [4]
-  uint64_t* full_v = full_k + kStages;                       // [4]
-  uint64_t* empty = full_v + kStages;                        // [4] the MMAs that read a stage are done
-  uint64_t* go = empty + kStages;                            // [4] the stage is the copying warps' to fill
+  uint8_t* sK = sP + 4 * kSlab;
+  uint8_t* sV = sK + kStages * kStage;
+  // Barriers.  A wait tells two neighbouring phases apart, no more, so each is
+  // waited on by roles that see all of its phases.
+  uint64_t* full_k = reinterpret_cast<uint64_t*>(sV + kStages * kStage);   // CTA 0: the parts of both CTAs are there
+  uint64_t* full_v = full_k + kStages;
+  uint64_t* empty_k = full_v + kStages;                      // the MMAs that read the stage are done
+  uint64_t* empty_v = empty_k + kStages;
+  uint64_t* go = empty_v + kStages;                          // the V stage is the copying warps' to fill
   uint64_t* q_full = go + kStages;                           // CTA 0: the queries of both CTAs
   uint64_t* q_free = q_full + 1;                             // the S products of an item are done
   uint64_t* o_free = q_free + 1;                             // CTA 0: an item's output is out of TMEM in both CTAs
@@ -276,8 +315,11 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
   const uint32_t cta = cta_rank();
   const int64_t n_clusters = gridDim.x >> 1, cluster = blockIdx.x >> 1;
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) { mbar_init(&full_k[i], 2); mbar_init(&full_v[i], 2); mbar_init(&empty[i], 1); mbar_init(&go[i], 1); }
-    for (int i = 0; i < kItems; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_free[i], 11); }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full_k[i], 2); mbar_init(&full_v[i], 2); mbar_init(&empty_k[i], 1); mbar_init(&empty_v[i], 1);
+      mbar_init(&go[i], 1);
+    }
+    for (int i = 0; i < kItems; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_free[i], 10); }
     mbar_init(q_full, 2); mbar_init(q_free, 1); mbar_init(o_free, 8);
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 8); }
     mbar_init(p_full, 8); mbar_init(pv_done, 1);
@@ -296,44 +338,60 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
   volatile int* abort_flag = s_abort;
 
   // Item k of this cluster, from the ring that warp 10 fills.  Whole-warp call; no
-  // item: the batch is done, or a wait expired.  The four warps of a role that
-  // shares a barrier (bar) get one answer.  The last reader of a role releases it.
-  auto next_item = [&](uint32_t k, Work& w, uint32_t bar, bool release) -> bool {
+  // item: the batch is done, or a wait expired.  The warps of a role that shares a
+  // named barrier (bar, of n threads) get one answer.
+  auto next_item = [&](uint32_t k, Work& w, uint32_t bar, uint32_t n) -> bool {
     const uint32_t sl = k % kItems;
     bool ok = wait_warp(&w_full[sl], (k / kItems) & 1, abort_flag);
-    if (bar != 0 && named_bar_or(bar, 128, !ok)) ok = false;
+    if (bar != 0 && named_bar_or(bar, n, !ok)) ok = false;
     if (!ok) return false;
     w = s_work[sl];
     __syncwarp();
-    if (release && lane == 0) mbar_arrive(&w_free[sl]);
+    if (lane == 0) mbar_arrive(&w_free[sl]);
     return w.has != 0;
   };
   auto tiles_of = [](const Work& w) { return (w.nb + kTileBlocks - 1) / kTileBlocks; };
-  // Stages in their order: K(0), K(1), then the stages of V(t) and K(t + 2) in turn
-  // for t = 0, 1, ...  K is 4 stages (dims 128 d ..), V one for each of the tile's
-  // blocks (the dims 256 j + 128 cta .. of j = 0, 1).  A stage has one arrival from
-  // each CTA.
   auto blocks_of = [](const Work& w, int i) { return min(kTileBlocks, w.nb - kTileBlocks * i); };
-
   // The tiles of all items in their order (items without rows have none).
   struct Stream {
     Work w;
     uint32_t k = 0, items = 0;   // items read; items with tiles so far, the present one included
     int i = 0, nt = 0;           // tile of the item
-    bool on = true;              // whether there is one
   };
-  auto advance = [&](Stream& x, uint32_t bar, bool release) {
-    if (++x.i < x.nt || !x.on) return;
+  auto advance = [&](Stream& x, uint32_t bar, uint32_t n) -> bool {
+    if (++x.i < x.nt) return true;
     do {
-      x.on = next_item(x.k++, x.w, bar, release);
-      if (!x.on) return;
+      if (!next_item(x.k++, x.w, bar, n)) return false;
       x.nt = tiles_of(x.w);
     } while (x.nt == 0);
     x.i = 0;
     ++x.items;
+    return true;
+  };
+  // Pages of less than 64 rows make several copies of a block: lane 4 kb + j of a
+  // producer has part j of block kb of a tile.
+  struct Part { int32_t y; int s, rows; bool on; };          // first row of the store, source, rows; whether there is one
+  auto part_of = [&](const Stream& x) {
+    const int kb = lane >> 2, j = lane & 3;
+    Part t{0, 0, kBlock, false};
+    if (kb < blocks_of(x.w, x.i)) {
+      int row;
+      t.s = block_at(x.w, kTileBlocks * x.i + kb, row);
+      const PageTable& pt = t.s ? p.pt[1] : p.pt[0];
+      t.rows = min(kBlock, 1 << pt.ps_log2);
+      t.on = j * t.rows < kBlock;
+      if (t.on) {
+        const int64_t g = page_row(pt, x.w.seq, row + j * t.rows);
+        // A part without a page reads page 0.  It has no visible row, so its logits
+        // are masked and its V is not loaded here; or the table is wrong.
+        if (g < 0 && block_clean(x.w, kTileBlocks * x.i + kb)) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
+        t.y = (int32_t)max((int64_t)0, g);
+      }
+    }
+    return t;
   };
 
-  if (warp == 7) {
+  if (warp == 10) {
     // ============================ items
     for (uint32_t k = 0;; ++k) {
       const uint32_t sl = k % kItems;
@@ -347,271 +405,182 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
       if (!w.has) break;
     }
   } else if (warp == 4) {
-    // ============================ TMA producer
-    // Lane 4 kb + j has part j of block kb of a tile: pages of less than 64 rows
-    // make several boxes of a block.  It looks its row of the page store up and
-    // issues the copies of its part itself.
+    // ============================ queries and K
+    const int kb = lane >> 2, j = lane & 3;
     uint32_t st = 0;                                         // stages so far
     bool ok = true;
-    const int kb = lane >> 2, j = lane & 3;
-    struct Part { int32_t y; int s, rows; bool on; };        // first row, source, rows; whether there is one
-    auto part_of = [&](const Stream& x) {
-      Part t{0, 0, kBlock, false};
-      if (x.on && kb < blocks_of(x.w, x.i)) {
-        int64_t row;
-        t.s = block_at(x.w, kTileBlocks * x.i + kb, row);
-        const PageTable& pt = t.s ? p.pt[1] : p.pt[0];
-        t.rows = min(kBlock, 1 << pt.ps_log2);
-        t.on = j * t.rows < kBlock;
-        if (t.on) {
-          const int64_t g = page_row(pt, x.w.seq, row + j * t.rows);
-          // A part without a page reads page 0.  It has no visible row, so its logits
-          // are masked and its V is not loaded here; or the table is wrong.
-          if (g < 0 && block_clean(x.w, kTileBlocks * x.i + kb)) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
-          t.y = (int32_t)max((int64_t)0, g);
+    Stream x;
+    while (ok && advance(x, 0, 0)) {
+      const Part t = part_of(x);
+      if (x.i == 0) {
+        ok = wait_warp(q_free, x.items & 1, abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          expect_leader(q_full, 8 * kSlab);
+          for (int s = 0; s < 8; ++s)
+            tma_load_pair(sQ + s * kSlab, &maps.q, 64 * s, (int32_t)((x.w.tok0 + (int64_t)cta * x.w.tpc) * p.H), q_full);
         }
+        __syncwarp();
       }
-      return t;
-    };
-    auto wait_empty = [&](uint32_t sl) {                     // one answer for the warp
-      ok = wait_warp(&empty[sl], ((st / kStages) & 1) ^ 1, abort_flag);
-      return ok;
-    };
-    auto load_q = [&](const Stream& x) {
-      ok = wait_warp(q_free, x.items & 1, abort_flag);
-      if (ok && lane == 0) {
-        expect_leader(q_full, 8 * kSlab);
-        for (int s = 0; s < 8; ++s)
-          tma_load_pair(sQ + s * kSlab, &map_q, 64 * s, (int32_t)((x.w.tok0 + (int64_t)cta * x.w.tpc) * p.H), q_full);
-      }
-      __syncwarp();
-    };
-    auto load_k = [&](const Stream& x, const Part& t, int d) {
       // blocks 2 cta, 2 cta + 1 of the tile; absent ones are not loaded (their logits are masked)
       const int n = max(0, min(2, blocks_of(x.w, x.i) - 2 * (int)cta));
-      const CUtensorMap* map = t.s ? &map_ent : &map_raw;
-      const uint32_t sl = st % kStages;
-      if (!wait_empty(sl)) return;
-      if (lane == 0) {
-        if (n) expect_leader(&full_k[sl], n * 2 * kSlab);
-        else arrive_leader(&full_k[sl]);
-      }
-      if (t.on && (kb >> 1) == (int)cta) {
-        uint8_t* dst = sRing + sl * kStage + (kb & 1) * kSlab + j * t.rows * 128;
-        tma_load_pair(dst, map, 128 * d, t.y, &full_k[sl]);
-        tma_load_pair(dst + 2 * kSlab, map, 128 * d + 64, t.y, &full_k[sl]);
-      }
-      ++st;
-    };
-    auto load_v = [&](const Stream& x, const Part& t, int v) {
-      const CUtensorMap* map = t.s ? &map_ent : &map_raw;
-      const uint32_t sl = st % kStages;
-      if (!wait_empty(sl)) return;
-      if (!block_clean(x.w, kTileBlocks * x.i + v)) {        // the copying warps'
-        if (lane == 0) mbar_arrive(&go[sl]);
-      } else {
-        if (lane == 0) expect_leader(&full_v[sl], kStage);
-        if (t.on && kb == v) {
-          uint8_t* dst = sRing + sl * kStage + j * t.rows * 128;
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            tma_load_pair(dst + h * kSlab, map, 256 * (h >> 1) + 128 * (int)cta + 64 * (h & 1), t.y, &full_v[sl]);
+      const bool mine = t.on && (kb >> 1) == (int)cta;
+      const CUtensorMap* map = t.s ? &maps.k[1] : &maps.k[0];
+      for (int d = 0; d < kKStages; ++d, ++st) {
+        const uint32_t sl = st % kStages;
+        ok = wait_warp(&empty_k[sl], ((st / kStages) & 1) ^ 1, abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          if (n) expect_leader(&full_k[sl], n * 2 * kSlab);
+          else arrive_leader(&full_k[sl]);
+        }
+        if (mine) {
+          uint8_t* dst = sK + sl * kStage + (kb & 1) * kSlab + j * t.rows * 128;
+          tma_load_pair(dst, map, 128 * d, t.y, &full_k[sl]);
+          tma_load_pair(dst + 2 * kSlab, map, 128 * d + 64, t.y, &full_k[sl]);
         }
       }
-      ++st;
-    };
-    Stream x0, x1, x2;                                       // tiles t, t + 1, t + 2
-    Part p0, p1, p2;
-    advance(x0, 0, true);
-    p0 = part_of(x0);
-    x1 = x0;
-    if (x0.on) load_q(x0);
-    for (int d = 0; d < kKStages && x0.on && ok; ++d) load_k(x0, p0, d);
-    advance(x1, 0, true);
-    p1 = part_of(x1);
-    x2 = x1;
-    if (x1.on && x1.i == 0 && ok) load_q(x1);
-    for (int d = 0; d < kKStages && x1.on && ok; ++d) load_k(x1, p1, d);
-    while (x0.on && ok) {
-      advance(x2, 0, true);
-      p2 = part_of(x2);
-      // the next item's queries, once S(t + 1) is done with the present ones
-      const bool q = x2.on && x2.i == 0;
-      for (int d = 0; d < kTileBlocks && ok; ++d) {
-        if (d < blocks_of(x0.w, x0.i)) load_v(x0, p0, d);
-        if (d == 0 && q && ok) load_q(x2);
-        if (x2.on && ok) load_k(x2, p2, d);
+    }
+  } else if (warp == 7) {
+    // ============================ V
+    const int kb = lane >> 2, j = lane & 3;
+    uint32_t st = 0;
+    bool ok = true;
+    Stream x;
+    while (ok && advance(x, 0, 0)) {
+      const Part t = part_of(x);
+      const CUtensorMap* map = t.s ? &maps.v[1] : &maps.v[0];
+      const int nbk = blocks_of(x.w, x.i);
+      for (int v = 0; v < nbk; ++v, ++st) {
+        const uint32_t sl = st % kStages;
+        ok = wait_warp(&empty_v[sl], ((st / kStages) & 1) ^ 1, abort_flag);
+        if (!ok) break;
+        if (!block_clean(x.w, kTileBlocks * x.i + v)) {      // the copying warps'
+          if (lane == 0) mbar_arrive(&go[sl]);
+          continue;
+        }
+        if (lane == 0) expect_leader(&full_v[sl], kStage);
+        if (t.on && kb == v) {
+          // a part's rows lie in all four slabs; with one part the block is one copy
+          uint8_t* dst = sV + sl * kStage + j * t.rows * 128;
+          if (t.rows == kBlock) {
+            tma_load_pair_4d(dst, map, 0, t.y, 2 * (int)cta, 0, &full_v[sl]);
+          } else {
+            const CUtensorMap* part = t.s ? &maps.k[1] : &maps.k[0];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              tma_load_pair(dst + h * kSlab, part, 256 * (h >> 1) + 128 * (int)cta + 64 * (h & 1), t.y, &full_v[sl]);
+          }
+        }
       }
-      x0 = x1; p0 = p1;
-      x1 = x2; p1 = p2;
     }
   } else if (warp >= 8) {
     // ============================ copies of V blocks that not every token sees
-    const int lt = tid - 256;                                // 0 .. 127
-    // They see few of the stages, so the phase of `empty` tells them nothing (a
-    // parity is ambiguous two phases on): the producer, which sees all of them,
+    const int lt = tid - 256;                                // 0 .. 63
+    // They see few of the stages, so `empty_v` tells them nothing: the producer
     // hands a stage over through its `go`, once for each use.
     uint32_t st = 0, uses = 0;                               // uses: bit sl, parity of the next use
     bool ok = true;
-    Stream x;                                                // tile t + 2
-    Work w0, w1;                                             // items of tiles t, t + 1
-    int i0, i1, nb0, nb1;                                    // their tiles of the item, and their blocks (0: no tile)
-    auto take = [&](Work& w, int& i, int& nb) {
-      w = x.w;
-      i = x.i;
-      nb = x.on ? blocks_of(x.w, x.i) : 0;
-    };
-    advance(x, 2, true);
-    take(w0, i0, nb0);
-    if (x.on) st += kKStages;
-    advance(x, 2, true);
-    take(w1, i1, nb1);
-    if (x.on) st += kKStages;
-    while (nb0 > 0 && ok) {
-      advance(x, 2, true);
-      const Work& w = w0;
-      const uint32_t step = x.on ? 2 : 1;                    // a K stage follows each V stage
-      for (int kb = 0; kb < nb0 && ok; ++kb) {
-        const uint32_t sv = st + step * kb;
-        const int i = i0;
-        if (block_clean(w, kTileBlocks * i + kb)) continue;
-        int64_t row0;
-        const int s = block_at(w, kTileBlocks * i + kb, row0);
+    Stream x;
+    while (ok && advance(x, 2, 64)) {
+      const int nbk = blocks_of(x.w, x.i);
+      for (int kb = 0; kb < nbk && ok; ++kb, ++st) {
+        if (block_clean(x.w, kTileBlocks * x.i + kb)) continue;
+        int row0;
+        const int s = block_at(x.w, kTileBlocks * x.i + kb, row0);
         const PageTable& pt = s ? p.pt[1] : p.pt[0];
         const __nv_bfloat16* store = static_cast<const __nv_bfloat16*>(s ? p.rows[1] : p.rows[0]);
-        const int64_t lo = s ? w.any_lo[1] : w.any_lo[0], hi = s ? w.any_hi[1] : w.any_hi[0];
-        const uint32_t sl = sv % kStages;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          // 64 rows x 128 dims: 16 pieces of 16 bytes a row, 16 lanes on a row
+        const int lo = s ? x.w.any_lo[1] : x.w.any_lo[0], hi = s ? x.w.any_hi[1] : x.w.any_hi[0];
+        const uint32_t sl = st % kStages;
+        // 64 rows x 256 dims: 16 pieces of 16 bytes a row and half, 16 lanes on a row
+#pragma unroll 1
+        for (int it = 0; it < 4; ++it) {
+          const int j = it >> 1, r0 = 32 * (it & 1);
           uint4 v[8];
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const int r = u * 8 + (lt >> 4), c = lt & 15;
-            const int64_t row = row0 + r;
+            const int r = r0 + u * 4 + (lt >> 4), c = lt & 15, row = row0 + r;
             v[u] = make_uint4(0, 0, 0, 0);
             if (row >= lo && row < hi) {
-              const int64_t g = page_row(pt, w.seq, row);
+              const int64_t g = page_row(pt, x.w.seq, row);
               if (g >= 0) v[u] = __ldg(reinterpret_cast<const uint4*>(store + g * kD + 256 * j + 128 * cta + 8 * c));
               else if (c == 0) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
             }
           }
-          if (j == 0) {
+          if (it == 0) {
             ok = wait_warp(&go[sl], (uses >> sl) & 1, abort_flag);
             uses ^= 1u << sl;
-            if (named_bar_or(2, 128, !ok)) ok = false;       // one answer for the four warps
+            if (named_bar_or(2, 64, !ok)) ok = false;        // one answer for the two warps
             if (!ok) break;
           }
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const int r = u * 8 + (lt >> 4), c = lt & 15;
+            const int r = r0 + u * 4 + (lt >> 4), c = lt & 15;
             v[u] = make_uint4(finite2(v[u].x), finite2(v[u].y), finite2(v[u].z), finite2(v[u].w));
-            st_shared16(smem_u32(sRing) + sl * kStage + (2 * j + (c >> 3)) * kSlab + swz128(r, c & 7), v[u]);
+            st_shared16(smem_u32(sV) + sl * kStage + (2 * j + (c >> 3)) * kSlab + swz128(r, c & 7), v[u]);
           }
         }
         if (!ok) break;
         fence_proxy_async_smem();
-        named_bar_sync(2, 128);
+        named_bar_sync(2, 64);
         if (lt == 0) arrive_leader(&full_v[sl]);
       }
-      st += nb0 + (x.on ? kKStages : 0);
-      w0 = w1;
-      i0 = i1;
-      nb0 = nb1;
-      take(w1, i1, nb1);
     }
-  } else if (warp == 5 || warp == 6) {
-    // ============================ MMA issuers: lane 0 of CTA 0, warp 5 of S, warp 6 of PV
-    const bool issue = cta == 0 && lane == 0;
+  } else if (warp == 5) {
+    // ============================ S (CTA 0)
+    const uint32_t idesc = make_idesc(128, 256, 1, 1, 0, 0);
+    const uint64_t dQ = smem_desc(smem_u32(sQ), 16, 1024, SWZ_128B);
+    const uint64_t dK = smem_desc(smem_u32(sK), 16, 1024, SWZ_128B);
     uint32_t st = 0, t = 0;                                  // stages and tiles so far
-    bool ok = true;
-    uint32_t uses = 0;                                       // bit sl: parity of this issuer's next use of slot sl
-    auto ready = [&](uint64_t* full, uint32_t sl) {
-      ok = ok && wait(&full[sl], (uses >> sl) & 1, abort_flag);
-      uses ^= 1u << sl;
-      tc_fence_after();
-      return ok;
-    };
-    Stream x;                                                // tile t + 2
-    auto blocks = [&]() { return x.on ? blocks_of(x.w, x.i) : 0; };
-    if (warp == 5) {
-      const uint32_t idesc = make_idesc(128, 256, 1, 1, 0, 0);
-      const uint64_t dQ = smem_desc(smem_u32(sQ), 16, 1024, SWZ_128B);
-      const uint64_t dK = smem_desc(smem_u32(sRing), 16, 1024, SWZ_128B);
-      // S of the stream's tile, number n; nv V stages alternate with its own
-      auto do_s = [&](uint32_t n, int nv) {
-        if (x.i == 0) ok = ok && wait(q_full, (x.items & 1) ^ 1, abort_flag);
-        ok = ok && wait(&s_free[n & 1], ((n >> 1) & 1) ^ 1, abort_flag);
-        for (int d = 0; d < kKStages && ok; ++d) {
-          const uint32_t sl = (st + d + min(d + 1, nv)) % kStages;
-          if (!ready(full_k, sl)) break;
+    bool ok = cta == 0;
+    Stream x;
+    for (; advance(x, 0, 0); ++t) {
+      if (ok && x.i == 0) ok = wait_warp(q_full, (x.items & 1) ^ 1, abort_flag);
+      ok = ok && wait_warp(&s_free[t & 1], ((t >> 1) & 1) ^ 1, abort_flag);
+      if (!ok) continue;
+      for (int d = 0; d < kKStages; ++d, ++st) {
+        const uint32_t sl = st % kStages;
+        ok = wait_warp(&full_k[sl], (st / kStages) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-          for (int m = 0; m < 8; ++m)
-            mma_pair(tmem + kSCol + 128 * (n & 1), dQ + (((2 * d + (m >> 2)) * kSlab + (m & 3) * 32) >> 4),
-                     dK + ((sl * kStage + (m >> 2) * 2 * kSlab + (m & 3) * 32) >> 4), idesc, (d | m) != 0);
-          commit_pair(&empty[sl]);
-        }
-        if (ok) {
-          commit_pair(&s_full[n & 1]);
-          if (x.i == x.nt - 1) commit_pair(q_free);
-        }
-      };
-      advance(x, 0, true);
-      int nb0 = blocks();
-      if (issue && x.on) do_s(0, 0);
-      if (x.on) st += kKStages;
-      __syncwarp();
-      advance(x, 0, true);
-      int nb1 = blocks();
-      if (issue && x.on) do_s(1, 0);
-      if (x.on) st += kKStages;
-      __syncwarp();
-      for (; nb0 > 0; ++t) {
-        advance(x, 0, true);
-        if (issue && x.on && ok) do_s(t + 2, nb0);
-        st += nb0 + (x.on ? kKStages : 0);
-        nb0 = nb1;
-        nb1 = blocks();
-        __syncwarp();
+        for (int m = 0; m < 8; ++m)
+          mma_pair(tmem + kSCol + 128 * (t & 1), dQ + (((2 * d + (m >> 2)) * kSlab + (m & 3) * 32) >> 4),
+                   dK + ((sl * kStage + (m >> 2) * 2 * kSlab + (m & 3) * 32) >> 4), idesc, (d | m) != 0);
+        commit_pair(&empty_k[sl]);
       }
-    } else {
-      const uint32_t idesc = make_idesc(128, 256, 1, 1, 0, 1);
-      const uint64_t dP = smem_desc(smem_u32(sP), 16, 1024, SWZ_128B);
-      const uint64_t dV = smem_desc(smem_u32(sRing), kSlab, 1024, SWZ_128B);
-      struct Tile { int i, items, nb; };
-      auto take = [&]() { return Tile{x.i, (int)x.items, blocks()}; };
-      advance(x, 0, true);
-      Tile t0 = take();
-      if (x.on) st += kKStages;
-      advance(x, 0, true);
-      Tile t1 = take();
-      if (x.on) st += kKStages;
-      for (; t0.nb > 0; ++t) {
-        advance(x, 0, true);
-        const uint32_t step = x.on ? 2 : 1;                  // a K stage follows each V stage
-        if (issue && ok) {
-          // O is overwritten at an item's first tile: the item before must be out of it
-          if (t0.i == 0) ok = ok && wait(o_free, t0.items & 1, abort_flag);
-          ok = ok && wait(p_full, t & 1, abort_flag);
-          for (int kb = 0; kb < t0.nb && ok; ++kb) {
-            const uint32_t sl = (st + step * kb) % kStages;
-            if (!ready(full_v, sl)) break;
-#pragma unroll
-            for (int m = 0; m < 8; ++m)
-              mma_pair(tmem + 128 * (m >> 2), dP + ((kb * kSlab + (m & 3) * 32) >> 4),
-                       dV + ((sl * kStage + (m >> 2) * 2 * kSlab + (m & 3) * 2048) >> 4), idesc,
-                       (t0.i | kb | (m & 3)) != 0);
-            commit_pair(&empty[sl]);
-          }
-          if (ok) commit_pair(pv_done);
-        }
-        st += t0.nb + (x.on ? kKStages : 0);
-        t0 = t1;
-        t1 = take();
-        __syncwarp();
+      if (ok) {
+        commit_pair(&s_full[t & 1]);
+        if (x.i == x.nt - 1) commit_pair(q_free);
       }
     }
-    __syncwarp();
+  } else if (warp == 6) {
+    // ============================ PV (CTA 0)
+    const uint32_t idesc = make_idesc(128, 256, 1, 1, 0, 1);
+    const uint64_t dP = smem_desc(smem_u32(sP), 16, 1024, SWZ_128B);
+    const uint64_t dV = smem_desc(smem_u32(sV), kSlab, 1024, SWZ_128B);
+    uint32_t st = 0, t = 0;
+    bool ok = cta == 0;
+    Stream x;
+    for (; advance(x, 0, 0); ++t) {
+      // O is overwritten at an item's first tile: the item before must be out of it
+      if (ok && x.i == 0) ok = wait_warp(o_free, x.items & 1, abort_flag);
+      ok = ok && wait_warp(p_full, t & 1, abort_flag);
+      if (!ok) continue;
+      const int nbk = blocks_of(x.w, x.i);
+      for (int kb = 0; kb < nbk; ++kb, ++st) {
+        const uint32_t sl = st % kStages;
+        ok = wait_warp(&full_v[sl], (st / kStages) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          mma_pair(tmem + 128 * (m >> 2), dP + ((kb * kSlab + (m & 3) * 32) >> 4),
+                   dV + ((sl * kStage + (m >> 2) * 2 * kSlab + (m & 3) * 2048) >> 4), idesc, (x.i | kb | (m & 3)) != 0);
+        commit_pair(&empty_v[sl]);
+      }
+      if (ok) commit_pair(pv_done);
+    }
   } else {
     // ============================ softmax and epilogue: lane tid of TMEM
     const int r = tid & 63, half = tid >> 6;
@@ -619,12 +588,12 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
     uint32_t g = 0, bc = 0;                                  // tiles and exchanges of the items before
     bool ok = true;
     Work w;
-    for (uint32_t k = 0; next_item(k, w, 1, true); ++k) {
+    for (uint32_t k = 0; next_item(k, w, 1, 128); ++k) {
       const int nt = tiles_of(w);
-      const int tk = (int)cta * w.tpc + r / p.H;               // this row's token of the pair
+      const int tk = (int)cta * w.tpc + r / p.H;             // this row's token of the pair
       const bool valid = r < w.tpc * p.H && tk < w.ntok && w.pos0 + tk >= 0;
       const int64_t pos = valid ? w.pos0 + tk : -1;
-      int64_t lo[2], hi[2];
+      int lo[2], hi[2];
       seen(p, 0, pos, lo[0], hi[0]);
       seen(p, 1, pos, lo[1], hi[1]);
       float m = -CUDART_INF_F, l = 0.f;
@@ -635,39 +604,40 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
         ok = ok && wait_warp(&s_full[t & 1], (t >> 1) & 1, abort_flag);
         tc_fence_after();
         const uint32_t ts = tmem + lane_base + kSCol + 128 * (t & 1);
-        // which of this thread's 128 columns (blocks 2 half, 2 half + 1) the row's token sees
+        // which of this thread's 128 columns (blocks 2 half, 2 half + 1) the row's
+        // token sees, and whether every row of the warp sees a whole block
         uint64_t see[2];
+        bool whole[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int kb = kTileBlocks * i + 2 * half + h;
           see[h] = 0;
           if (kb < w.nb) {
-            int64_t row;
+            int row;
             const int s = block_at(w, kb, row);
-            const int64_t a = (s ? lo[1] : lo[0]) - row, e = (s ? hi[1] : hi[0]) - row;   // visible: [a, e) of the block
+            const int a = (s ? lo[1] : lo[0]) - row, e = (s ? hi[1] : hi[0]) - row;   // visible: [a, e) of the block
             const uint64_t below = e >= 64 ? ~0ull : e <= 0 ? 0ull : (1ull << e) - 1;
             const uint64_t from = a <= 0 ? ~0ull : a >= 64 ? 0ull : ~((1ull << a) - 1);
             see[h] = below & from;
           }
+          whole[h] = __all_sync(0xffffffffu, see[h] == ~0ull);
         }
-        // whether every row of the warp sees all 64 columns of a block
-        const bool whole[2] = {__all_sync(0xffffffffu, see[0] == ~0ull) != 0, __all_sync(0xffffffffu, see[1] == ~0ull) != 0};
         // pass 1: the maximum of the visible logits
         float mx = -CUDART_INF_F;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int h = 0; h < 2; ++h) {
           if (!ok) break;
-          float x[32];
-          tmem_ld32(ts + 32 * c, x);
+          float x[64];
+          tmem_ld32(ts + 64 * h, x);
+          tmem_ld32(ts + 64 * h + 32, x + 32);
           tmem_wait_ld();
-          if (!whole[c >> 1]) {
-            const uint32_t bits = (uint32_t)(see[c >> 1] >> (32 * (c & 1)));
+          if (!whole[h]) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = (bits >> k) & 1u ? x[k] : -CUDART_INF_F;
+            for (int q = 0; q < 64; ++q) x[q] = (see[h] >> q) & 1u ? x[q] : -CUDART_INF_F;
           }
           float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int k = 4; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], x[k]);
+          for (int q = 4; q < 64; ++q) m4[q & 3] = fmaxf(m4[q & 3], x[q]);
           mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
         }
         float* sx = s_x + (bc++ & 1) * 128;
@@ -678,65 +648,66 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
         // The maximum moves only when it grows by more than 2^kTau.
         float alpha = 1.f;
         if (mx > m + kTau) {
-          alpha = exp2f(m - mx);                               // 0 the first time
+          alpha = exp2f(m - mx);                             // 0 the first time
           m = mx;
         }
         l *= alpha;
-      const float ref = m == -CUDART_INF_F ? 0.f : m;
-      // pass 2: probabilities, as bf16 pairs in registers
-      uint32_t pk[64];
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        // pass 2: probabilities, as bf16 pairs in registers
+        uint32_t pk[64];
+        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float x[32];
-        tmem_ld32(ts + 32 * c, x);
-        tmem_wait_ld();
-        if (!whole[c >> 1]) {
-          // a visible logit of -inf is a non-finite row's, whose V may read as zeros
-          const uint32_t bits = (uint32_t)(see[c >> 1] >> (32 * (c & 1)));
+        for (int h = 0; h < 2; ++h) {
+          float x[64];
+          tmem_ld32(ts + 64 * h, x);
+          tmem_ld32(ts + 64 * h + 32, x + 32);
+          tmem_wait_ld();
+          if (!whole[h]) {
+            // a visible logit of -inf is a non-finite row's, whose V may read as zeros
 #pragma unroll
-          for (int q = 0; q < 32; ++q)
-            x[q] = !((bits >> q) & 1u) ? -CUDART_INF_F : x[q] == -CUDART_INF_F ? CUDART_NAN_F : x[q];
-        }
-#pragma unroll
-        for (int q = 0; q < 32; ++q) x[q] = exp2_fast(fmaf(x[q], p.scale_log2, -ref));
-#pragma unroll
-        for (int q = 0; q < 32; ++q) l4[q & 3] += x[q];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) pk[16 * c + q] = pack2(x[2 * q], x[2 * q + 1]);
-      }
-      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_leader(&s_free[t & 1]);
-      // P and O are free once PV(t - 1) is done (of an earlier item: its epilogue waited)
-      if (i > 0) {
-        ok = wait_warp(pv_done, (t - 1) & 1, abort_flag);
-        if (!ok) continue;
-        tc_fence_after();
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-          for (int c = 0; c < 16; ++c) {
-            float o[16];
-            tmem_ld16(tmem + lane_base + 16 * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] *= alpha;
-            tmem_st16(tmem + lane_base + 16 * c, o);
+            for (int q = 0; q < 64; ++q)
+              x[q] = !((see[h] >> q) & 1u) ? -CUDART_INF_F : x[q] == -CUDART_INF_F ? CUDART_NAN_F : x[q];
           }
-          tmem_wait_st();
-          tc_fence_before();
-        }
-      }
-      const uint32_t pb = smem_u32(sP) + (2 * half) * kSlab;
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        st_shared16(pb + (q >> 3) * kSlab + swz128(r, q & 7), make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_leader(p_full);
-    }
-    // ---------------- epilogue
+          for (int q = 0; q < 32; ++q) {
+            const float2 z = fma2(make_float2(x[2 * q], x[2 * q + 1]), make_float2(p.scale_log2, p.scale_log2), make_float2(-ref, -ref));
+            const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+            l2[q & 1] = add2(l2[q & 1], e);
+            pk[32 * h + q] = pack2(e.x, e.y);
+          }
+        }
+        l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(&s_free[t & 1]);
+        // P and O are free once PV(t - 1) is done (of an earlier item: its epilogue waited)
+        if (i > 0) {
+          ok = wait_warp(pv_done, (t - 1) & 1, abort_flag);
+          if (!ok) continue;
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              float o[16];
+              tmem_ld16(tmem + lane_base + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] *= alpha;
+              tmem_st16(tmem + lane_base + 16 * c, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+        }
+        const uint32_t pb = smem_u32(sP) + (2 * half) * kSlab;
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          st_shared16(pb + (q >> 3) * kSlab + swz128(r, q & 7), make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_leader(p_full);
+      }
+      // ---------------- epilogue
       {
         float* sx = s_x + (bc++ & 1) * 128;
         sx[half * 64 + r] = l;
@@ -826,18 +797,24 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtens
 }  // namespace
 
 csa_status_t launch_paged_pair(PairParams& p, cudaStream_t st) {
-  CUtensorMap maps[3];
-  memset(maps, 0, sizeof(maps));
-  if (!encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.q, kD, p.n_tok * p.H, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+  PairMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (!encode_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.q, kD, p.n_tok * p.H, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
     return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (queries) failed");
   for (int s = 0; s < 2; ++s) {
     if (!p.rows[s]) continue;
     const int ps = 1 << p.pt[s].ps_log2;
-    if (!encode_2d(&maps[1 + s], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.rows[s], kD, p.pt[s].n_pages * ps, 64,
-                   std::min(ps, kBlock), CU_TENSOR_MAP_SWIZZLE_128B))
+    const cuuint64_t rows = (cuuint64_t)p.pt[s].n_pages * ps;
+    const cuuint32_t box_rows = (cuuint32_t)std::min(ps, kBlock);
+    const cuuint64_t dims[4] = {64, rows, 4, 2}, strides[3] = {kD * 2, 128, 512};
+    const cuuint32_t box[4] = {64, box_rows, 2, 2}, step[4] = {1, 1, 1, 1};
+    if (!encode_2d(&maps.k[s], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.rows[s], kD, rows, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        tmap_encoder()(&maps.v[s], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.rows[s]), dims, strides, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (pages) failed");
   }
-  const size_t smem = 1024 + 12 * kSlab + kStages * kStage + (4 * kStages + 9 + 2 * kItems) * 8 + 256 * 4 + 16;
+  const size_t smem = 1024 + 12 * kSlab + 2 * kStages * kStage + (5 * kStages + 9 + 2 * kItems) * 8 + 256 * 4 + 16;
   cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
   // Every sequence's last tile may be partly filled: an upper bound of the tiles
@@ -846,7 +823,7 @@ csa_status_t launch_paged_pair(PairParams& p, cudaStream_t st) {
   if (tiles > 0x3fffffff) return fail(CSA_ERR_UNSUPPORTED, "csa_paged_attention: too many tokens");
   // one cluster for every two SMs (one CTA fits an SM)
   const int64_t clusters = std::min<int64_t>(tiles, num_sms() / 2);
-  e = launch_pdl(pair_kernel, dim3((unsigned)(2 * clusters)), dim3(kThreads), smem, st, p, maps[0], maps[1], maps[2]);
+  e = launch_pdl(pair_kernel, dim3((unsigned)(2 * clusters)), dim3(kThreads), smem, st, p, maps);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: launch failed: %s", cudaGetErrorString(e));
   return check_launch("csa_paged_attention");
 }
