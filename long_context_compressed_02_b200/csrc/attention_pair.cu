@@ -19,9 +19,11 @@
 // K and V stream through a ring of two 32 KB stages each (8 MMAs a stage): K as
 // 128 rows x 128 dims, V as 64 rows x 256 dims.  Each has a producer and an
 // issuer of its own (one thread cannot issue the copies of both, at about 100
-// cycles a copy).  PV(t) runs next to S(t + 2), and
-// the softmax of tile t + 1 under both: it holds its probabilities in registers
-// until PV(t) is done with P.
+// cycles a copy).  PV(t) runs next to S(t + 2), and the softmax of tile t + 1
+// under both: it takes its logits out of TMEM at once and holds its probabilities
+// in registers until PV(t) is done with P.  Eight warps share it, two on each
+// scheduler, so that one's waits cover the other's (with four, a tile took 5,400
+// cycles and the tensor pipe waited for it).
 //
 // Clusters are persistent and take every n-th pair of token groups (an item).
 // Tiles follow one another over the items, and one warp looks the items up ahead
@@ -31,10 +33,10 @@
 // Rows that some tokens of the pair see and others do not (the ends of a window,
 // the causal diagonal, an unfilled block) need care where they may hold NaN or
 // were never written: the logits of the tokens that do not see them are masked,
-// but their zero probability times a NaN is a NaN.  Such V blocks are not loaded
-// by TMA: loader warps copy the visible rows, with non-finite elements as zeros
-// (a token that does see the row gets its NaN from the logits), and zeros for
-// the others.
+// but their zero probability times a NaN is a NaN.  Two warps patch such V blocks
+// in shared memory before the MMAs read them: rows that no token sees become
+// zeros, and in rows that some see non-finite elements do (a token that does see
+// the row gets its NaN from the logits).
 #include <algorithm>
 #include <cstring>
 #include <cuda_bf16.h>
@@ -64,9 +66,10 @@ constexpr int kStages = 2;                 // of each ring
 constexpr uint32_t kStage = 32768;         // K: [2 x 64 dims][128 rows], V: [4 x 64 dims][64 rows]
 constexpr int kKStages = 4;                // stages of a tile's K; its V has one for each block
 constexpr uint32_t kSlab = 8192;           // 64 rows x 128 bytes
-// warps 0-3 softmax and output, 4 loads Q and K, 7 loads V, 5 issues S and 6 PV
-// (in CTA 0), 8 and 9 copy V blocks, 10 looks up items
-constexpr int kThreads = 352;
+// warps 0-7 softmax and output, 8 loads Q and K, 11 loads V, 9 issues S and 10 PV
+// (in CTA 0), 12 and 13 patch V blocks, 14 looks up items
+constexpr int kThreads = 480;
+constexpr int kSoft = 256;                 // threads of the softmax
 constexpr float kTau = 8.0f;               // lazy-rescale threshold (log2 units)
 constexpr uint32_t kSCol = 256;            // S buffers behind the 256 columns of O
 constexpr int kItems = 4;                  // items that are looked up ahead
@@ -124,6 +127,14 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
 // The same for a whole warp, with one answer.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, wait(bar, parity, abort_flag));
+}
+// A V block's copy in this CTA alone, completing on a barrier of its own.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, int32_t u,
+                                           uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+               " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+               :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u),
+                  "r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void tma_load_pair_4d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
                                                 int32_t u, uint64_t* bar) {
@@ -205,7 +216,8 @@ __device__ __forceinline__ void seen(const PairParams& p, int s, int64_t pos, in
     hi = (int)min(p.cap[0], pos + 1);
     lo = p.W == 0 ? 0 : (int)min((int64_t)hi, max((int64_t)0, pos - p.W + 1));
   } else {
-    hi = (int)min(p.cap[1], (pos + 1) / p.m);
+    const int64_t n = pos < 0x7fffffff ? (int64_t)((uint32_t)(pos + 1) / (uint32_t)p.m) : (pos + 1) / p.m;
+    hi = (int)min(p.cap[1], n);
   }
 }
 // Source and first row of block kb.
@@ -282,10 +294,13 @@ __device__ __forceinline__ void find_work(const PairParams& p, int64_t x, int la
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMaps maps) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];          // the kernel has no other shared memory
   pdl_wait();
   pdl_trigger();
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  if (smem_u32(smem) & 1023u) {                              // the swizzled slabs start on 1024 bytes
+    if (threadIdx.x == 0) atomicOr(&g_err_pair, DEV_ERR_TIMEOUT_MBAR);
+    return;
+  }
   uint8_t* sQ = smem;                                        // [8 slabs][64 rows][128 B]
   uint8_t* sP = sQ + 8 * kSlab;                              // [4 slabs][64 rows][128 B]
   uint8_t* sK = sP + 4 * kSlab;
@@ -296,8 +311,8 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
   uint64_t* full_v = full_k + kStages;
   uint64_t* empty_k = full_v + kStages;                      // the MMAs that read the stage are done
   uint64_t* empty_v = empty_k + kStages;
-  uint64_t* go = empty_v + kStages;                          // the V stage is the copying warps' to fill
-  uint64_t* q_full = go + kStages;                           // CTA 0: the queries of both CTAs
+  uint64_t* patch = empty_v + kStages;                       // this CTA's part of the V stage is there, to be patched
+  uint64_t* q_full = patch + kStages;                           // CTA 0: the queries of both CTAs
   uint64_t* q_free = q_full + 1;                             // the S products of an item are done
   uint64_t* o_free = q_free + 1;                             // CTA 0: an item's output is out of TMEM in both CTAs
   uint64_t* w_full = o_free + 1;                             // [4] an item is in s_work ...
@@ -306,10 +321,10 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
   uint64_t* s_free = s_full + 2;                             // [2] CTA 0: read by the softmax of both CTAs
   uint64_t* p_full = s_free + 2;                             // CTA 0: P and the rescaled O of both CTAs
   uint64_t* pv_done = p_full + 1;
-  float* s_x = reinterpret_cast<float*>(pv_done + 1);        // [2][2][64] maxima / sums of the row halves
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_x + 256);
+  float* s_x = reinterpret_cast<float*>(pv_done + 1);        // [2][4][64] maxima / sums of the row quarters
+  Work* s_work = reinterpret_cast<Work*>(s_x + 512);         // [4]
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_work + kItems);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
-  __shared__ Work s_work[kItems];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t cta = cta_rank();
@@ -317,16 +332,16 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full_k[i], 2); mbar_init(&full_v[i], 2); mbar_init(&empty_k[i], 1); mbar_init(&empty_v[i], 1);
-      mbar_init(&go[i], 1);
+      mbar_init(&patch[i], 1);
     }
-    for (int i = 0; i < kItems; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_free[i], 10); }
-    mbar_init(q_full, 2); mbar_init(q_free, 1); mbar_init(o_free, 8);
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 8); }
-    mbar_init(p_full, 8); mbar_init(pv_done, 1);
+    for (int i = 0; i < kItems; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_free[i], 14); }
+    mbar_init(q_full, 2); mbar_init(q_free, 1); mbar_init(o_free, 16);
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 16); }
+    mbar_init(p_full, 16); mbar_init(pv_done, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(s_tmem)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
@@ -337,7 +352,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
   const uint32_t tmem = *s_tmem;
   volatile int* abort_flag = s_abort;
 
-  // Item k of this cluster, from the ring that warp 10 fills.  Whole-warp call; no
+  // Item k of this cluster, from the ring that warp 14 fills.  Whole-warp call; no
   // item: the batch is done, or a wait expired.  The warps of a role that shares a
   // named barrier (bar, of n threads) get one answer.
   auto next_item = [&](uint32_t k, Work& w, uint32_t bar, uint32_t n) -> bool {
@@ -383,15 +398,17 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       if (t.on) {
         const int64_t g = page_row(pt, x.w.seq, row + j * t.rows);
         // A part without a page reads page 0.  It has no visible row, so its logits
-        // are masked and its V is not loaded here; or the table is wrong.
-        if (g < 0 && block_clean(x.w, kTileBlocks * x.i + kb)) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
+        // are masked and its V is patched; or the table is wrong.
+        if (g < 0 && row + j * t.rows < (t.s ? x.w.any_hi[1] : x.w.any_hi[0]) &&
+            row + (j + 1) * t.rows > (t.s ? x.w.any_lo[1] : x.w.any_lo[0]))
+          atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
         t.y = (int32_t)max((int64_t)0, g);
       }
     }
     return t;
   };
 
-  if (warp == 10) {
+  if (warp == 14) {
     // ============================ items
     for (uint32_t k = 0;; ++k) {
       const uint32_t sl = k % kItems;
@@ -404,7 +421,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       }
       if (!w.has) break;
     }
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ============================ queries and K
     const int kb = lane >> 2, j = lane & 3;
     uint32_t st = 0;                                         // stages so far
@@ -441,7 +458,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
         }
       }
     }
-  } else if (warp == 7) {
+  } else if (warp == 11) {
     // ============================ V
     const int kb = lane >> 2, j = lane & 3;
     uint32_t st = 0;
@@ -450,83 +467,72 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
     while (ok && advance(x, 0, 0)) {
       const Part t = part_of(x);
       const CUtensorMap* map = t.s ? &maps.v[1] : &maps.v[0];
+      const CUtensorMap* part = t.s ? &maps.k[1] : &maps.k[0];
       const int nbk = blocks_of(x.w, x.i);
       for (int v = 0; v < nbk; ++v, ++st) {
         const uint32_t sl = st % kStages;
         ok = wait_warp(&empty_v[sl], ((st / kStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
-        if (!block_clean(x.w, kTileBlocks * x.i + v)) {      // the copying warps'
-          if (lane == 0) mbar_arrive(&go[sl]);
-          continue;
+        const bool clean = block_clean(x.w, kTileBlocks * x.i + v);
+        if (lane == 0) {
+          if (clean) expect_leader(&full_v[sl], kStage);
+          else mbar_expect_tx(&patch[sl], kStage);
         }
-        if (lane == 0) expect_leader(&full_v[sl], kStage);
         if (t.on && kb == v) {
-          // a part's rows lie in all four slabs; with one part the block is one copy
+          // the block's rows lie in all four slabs: one copy, or one for each part and slab
           uint8_t* dst = sV + sl * kStage + j * t.rows * 128;
           if (t.rows == kBlock) {
-            tma_load_pair_4d(dst, map, 0, t.y, 2 * (int)cta, 0, &full_v[sl]);
+            if (clean) tma_load_pair_4d(dst, map, 0, t.y, 2 * (int)cta, 0, &full_v[sl]);
+            else tma_load_4d(dst, map, 0, t.y, 2 * (int)cta, 0, &patch[sl]);
           } else {
-            const CUtensorMap* part = t.s ? &maps.k[1] : &maps.k[0];
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-              tma_load_pair(dst + h * kSlab, part, 256 * (h >> 1) + 128 * (int)cta + 64 * (h & 1), t.y, &full_v[sl]);
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              const int d = 256 * (h >> 1) + 128 * (int)cta + 64 * (h & 1);
+              if (clean) tma_load_pair(dst + h * kSlab, part, d, t.y, &full_v[sl]);
+              else tma_load_2d(dst + h * kSlab, part, d, t.y, &patch[sl]);
+            }
           }
         }
       }
     }
-  } else if (warp >= 8) {
-    // ============================ copies of V blocks that not every token sees
-    const int lt = tid - 256;                                // 0 .. 63
-    // They see few of the stages, so `empty_v` tells them nothing: the producer
-    // hands a stage over through its `go`, once for each use.
+  } else if (warp == 12 || warp == 13) {
+    // ============================ patches of V blocks that not every token sees
+    const int lt = tid - 384;                                // 0 .. 63: row of the block
     uint32_t st = 0, uses = 0;                               // uses: bit sl, parity of the next use
     bool ok = true;
     Stream x;
     while (ok && advance(x, 2, 64)) {
       const int nbk = blocks_of(x.w, x.i);
-      for (int kb = 0; kb < nbk && ok; ++kb, ++st) {
+      for (int kb = 0; kb < nbk; ++kb, ++st) {
         if (block_clean(x.w, kTileBlocks * x.i + kb)) continue;
-        int row0;
-        const int s = block_at(x.w, kTileBlocks * x.i + kb, row0);
-        const PageTable& pt = s ? p.pt[1] : p.pt[0];
-        const __nv_bfloat16* store = static_cast<const __nv_bfloat16*>(s ? p.rows[1] : p.rows[0]);
-        const int lo = s ? x.w.any_lo[1] : x.w.any_lo[0], hi = s ? x.w.any_hi[1] : x.w.any_hi[0];
+        int row;
+        const int s = block_at(x.w, kTileBlocks * x.i + kb, row);
+        row += lt;
+        const bool any = row >= (s ? x.w.any_lo[1] : x.w.any_lo[0]) && row < (s ? x.w.any_hi[1] : x.w.any_hi[0]);
+        const bool all = row >= (s ? x.w.all_lo[1] : x.w.all_lo[0]) && row < (s ? x.w.all_hi[1] : x.w.all_hi[0]);
         const uint32_t sl = st % kStages;
-        // 64 rows x 256 dims: 16 pieces of 16 bytes a row and half, 16 lanes on a row
-#pragma unroll 1
-        for (int it = 0; it < 4; ++it) {
-          const int j = it >> 1, r0 = 32 * (it & 1);
-          uint4 v[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int r = r0 + u * 4 + (lt >> 4), c = lt & 15, row = row0 + r;
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (row >= lo && row < hi) {
-              const int64_t g = page_row(pt, x.w.seq, row);
-              if (g >= 0) v[u] = __ldg(reinterpret_cast<const uint4*>(store + g * kD + 256 * j + 128 * cta + 8 * c));
-              else if (c == 0) atomicOr(&g_err_pair, DEV_ERR_BAD_INDEX);
+        ok = wait_warp(&patch[sl], (uses >> sl) & 1, abort_flag);
+        uses ^= 1u << sl;
+        if (named_bar_or(2, 64, !ok)) ok = false;            // one answer for the two warps
+        if (!ok) break;
+        if (!all) {
+#pragma unroll 4
+          for (int q = 0; q < 32; ++q) {                     // the row's 32 pieces of 16 bytes
+            uint8_t* at = sV + sl * kStage + (q >> 3) * kSlab + swz128(lt, (q + lt) & 7);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (any) {
+              v = *reinterpret_cast<const uint4*>(at);
+              v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
             }
-          }
-          if (it == 0) {
-            ok = wait_warp(&go[sl], (uses >> sl) & 1, abort_flag);
-            uses ^= 1u << sl;
-            if (named_bar_or(2, 64, !ok)) ok = false;        // one answer for the two warps
-            if (!ok) break;
-          }
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int r = r0 + u * 4 + (lt >> 4), c = lt & 15;
-            v[u] = make_uint4(finite2(v[u].x), finite2(v[u].y), finite2(v[u].z), finite2(v[u].w));
-            st_shared16(smem_u32(sV) + sl * kStage + (2 * j + (c >> 3)) * kSlab + swz128(r, c & 7), v[u]);
+            st_shared16(smem_u32(at), v);
           }
         }
-        if (!ok) break;
         fence_proxy_async_smem();
         named_bar_sync(2, 64);
         if (lt == 0) arrive_leader(&full_v[sl]);
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ============================ S (CTA 0)
     const uint32_t idesc = make_idesc(128, 256, 1, 1, 0, 0);
     const uint64_t dQ = smem_desc(smem_u32(sQ), 16, 1024, SWZ_128B);
@@ -554,7 +560,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
         if (x.i == x.nt - 1) commit_pair(q_free);
       }
     }
-  } else if (warp == 6) {
+  } else if (warp == 10) {
     // ============================ PV (CTA 0)
     const uint32_t idesc = make_idesc(128, 256, 1, 1, 0, 1);
     const uint64_t dP = smem_desc(smem_u32(sP), 16, 1024, SWZ_128B);
@@ -582,13 +588,16 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       if (ok) commit_pair(pv_done);
     }
   } else {
-    // ============================ softmax and epilogue: lane tid of TMEM
-    const int r = tid & 63, half = tid >> 6;
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    // ============================ softmax and epilogue
+    // Warp w reads lanes 32 (w % 4) .. of TMEM: row r of the CTA, half `half` of an
+    // accumulator's columns; and of the 128 columns of an S buffer there the 64 of
+    // block 2 half + cg, cg = w / 4.
+    const int r = tid & 63, half = (warp >> 1) & 1, cg = warp >> 2;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t g = 0, bc = 0;                                  // tiles and exchanges of the items before
     bool ok = true;
     Work w;
-    for (uint32_t k = 0; next_item(k, w, 1, 128); ++k) {
+    for (uint32_t k = 0; next_item(k, w, 1, kSoft); ++k) {
       const int nt = tiles_of(w);
       const int tk = (int)cta * w.tpc + r / p.H;             // this row's token of the pair
       const bool valid = r < w.tpc * p.H && tk < w.ntok && w.pos0 + tk >= 0;
@@ -601,50 +610,46 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       // waits for another for ever.
       for (int i = 0; i < nt; ++i) {
         const uint32_t t = g + i;
+        // the columns of the block that the row's token sees: [a, e)
+        const int kb = kTileBlocks * i + 2 * half + cg;
+        int a = 0, e = 0;
+        if (kb < w.nb) {
+          int row;
+          const int s = block_at(w, kb, row);
+          a = (s ? lo[1] : lo[0]) - row;
+          e = (s ? hi[1] : hi[0]) - row;
+        }
+        const bool whole = __all_sync(0xffffffffu, a <= 0 && e >= kBlock);
         ok = ok && wait_warp(&s_full[t & 1], (t >> 1) & 1, abort_flag);
-        tc_fence_after();
-        const uint32_t ts = tmem + lane_base + kSCol + 128 * (t & 1);
-        // which of this thread's 128 columns (blocks 2 half, 2 half + 1) the row's
-        // token sees, and whether every row of the warp sees a whole block
-        uint64_t see[2];
-        bool whole[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int kb = kTileBlocks * i + 2 * half + h;
-          see[h] = 0;
-          if (kb < w.nb) {
-            int row;
-            const int s = block_at(w, kb, row);
-            const int a = (s ? lo[1] : lo[0]) - row, e = (s ? hi[1] : hi[0]) - row;   // visible: [a, e) of the block
-            const uint64_t below = e >= 64 ? ~0ull : e <= 0 ? 0ull : (1ull << e) - 1;
-            const uint64_t from = a <= 0 ? ~0ull : a >= 64 ? 0ull : ~((1ull << a) - 1);
-            see[h] = below & from;
-          }
-          whole[h] = __all_sync(0xffffffffu, see[h] == ~0ull);
-        }
-        // pass 1: the maximum of the visible logits
-        float mx = -CUDART_INF_F;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!ok) break;
-          float x[64];
-          tmem_ld32(ts + 64 * h, x);
-          tmem_ld32(ts + 64 * h + 32, x + 32);
+        float x[64];
+        if (ok) {
+          tc_fence_after();
+          const uint32_t ts = tmem + lane_base + kSCol + 128 * (t & 1) + 64 * cg;
+          tmem_ld32(ts, x);
+          tmem_ld32(ts + 32, x + 32);
           tmem_wait_ld();
-          if (!whole[h]) {
-#pragma unroll
-            for (int q = 0; q < 64; ++q) x[q] = (see[h] >> q) & 1u ? x[q] : -CUDART_INF_F;
-          }
-          float m4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-          for (int q = 4; q < 64; ++q) m4[q & 3] = fmaxf(m4[q & 3], x[q]);
-          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader(&s_free[t & 1]);
         }
-        float* sx = s_x + (bc++ & 1) * 128;
-        sx[half * 64 + r] = mx;
-        if (named_bar_or(1, 128, !ok)) ok = false;
+        bool nan = false;
+        if (!whole) {
+          // a visible logit of -inf is a non-finite row's, whose V may read as zeros
+#pragma unroll
+          for (int q = 0; q < 64; ++q) {
+            const bool on = q >= a && q < e;
+            nan |= on && x[q] == -CUDART_INF_F;
+            x[q] = on ? x[q] : -CUDART_INF_F;
+          }
+        }
+        float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int q = 4; q < 64; ++q) m4[q & 3] = fmaxf(m4[q & 3], x[q]);
+        float* sx = s_x + (bc++ & 1) * 256;
+        sx[64 * (2 * half + cg) + r] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        if (named_bar_or(1, kSoft, !ok)) ok = false;
         if (!ok) continue;
-        mx = fmaxf(sx[r], sx[64 + r]) * p.scale_log2;
+        const float mx = fmaxf(fmaxf(sx[r], sx[64 + r]), fmaxf(sx[128 + r], sx[192 + r])) * p.scale_log2;
         // The maximum moves only when it grows by more than 2^kTau.
         float alpha = 1.f;
         if (mx > m + kTau) {
@@ -652,128 +657,112 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
           m = mx;
         }
         l *= alpha;
-        const float ref = m == -CUDART_INF_F ? 0.f : m;
-        // pass 2: probabilities, as bf16 pairs in registers
-        uint32_t pk[64];
+        const float ref = nan ? CUDART_NAN_F : m == -CUDART_INF_F ? 0.f : m;
+        // probabilities, as bf16 pairs in registers
+        uint32_t pk[32];
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float x[64];
-          tmem_ld32(ts + 64 * h, x);
-          tmem_ld32(ts + 64 * h + 32, x + 32);
-          tmem_wait_ld();
-          if (!whole[h]) {
-            // a visible logit of -inf is a non-finite row's, whose V may read as zeros
-#pragma unroll
-            for (int q = 0; q < 64; ++q)
-              x[q] = !((see[h] >> q) & 1u) ? -CUDART_INF_F : x[q] == -CUDART_INF_F ? CUDART_NAN_F : x[q];
-          }
-#pragma unroll
-          for (int q = 0; q < 32; ++q) {
-            const float2 z = fma2(make_float2(x[2 * q], x[2 * q + 1]), make_float2(p.scale_log2, p.scale_log2), make_float2(-ref, -ref));
-            const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-            l2[q & 1] = add2(l2[q & 1], e);
-            pk[32 * h + q] = pack2(e.x, e.y);
-          }
+        for (int q = 0; q < 32; ++q) {
+          const float2 z = fma2(make_float2(x[2 * q], x[2 * q + 1]), make_float2(p.scale_log2, p.scale_log2), make_float2(-ref, -ref));
+          const float2 y = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+          l2[q & 1] = add2(l2[q & 1], y);
+          pk[q] = pack2(y.x, y.y);
         }
         l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_leader(&s_free[t & 1]);
         // P and O are free once PV(t - 1) is done (of an earlier item: its epilogue waited)
         if (i > 0) {
           ok = wait_warp(pv_done, (t - 1) & 1, abort_flag);
           if (!ok) continue;
           tc_fence_after();
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {       // this warp's 128 columns of O
 #pragma unroll 1
-            for (int c = 0; c < 16; ++c) {
-              float o[16];
-              tmem_ld16(tmem + lane_base + 16 * c, o);
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              const uint32_t to = tmem + lane_base + 128 * cg + 32 * c;
+              tmem_ld32(to, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < 16; ++q) o[q] *= alpha;
-              tmem_st16(tmem + lane_base + 16 * c, o);
+              for (int q = 0; q < 32; ++q) o[q] *= alpha;
+              tmem_st16(to, o);
+              tmem_st16(to + 16, o + 16);
             }
             tmem_wait_st();
             tc_fence_before();
           }
         }
-        const uint32_t pb = smem_u32(sP) + (2 * half) * kSlab;
+        const uint32_t pb = smem_u32(sP) + (2 * half + cg) * kSlab;
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
-          st_shared16(pb + (q >> 3) * kSlab + swz128(r, q & 7), make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
+        for (int q = 0; q < 8; ++q)
+          st_shared16(pb + swz128(r, q), make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_leader(p_full);
       }
       // ---------------- epilogue
-      {
-        float* sx = s_x + (bc++ & 1) * 128;
-        sx[half * 64 + r] = l;
-        named_bar_sync(1, 128);
-        l = sx[r] + sx[64 + r];
-        float coef = 0.f;
-        if (valid) {
-          const float sk = p.sink ? p.sink[r % p.H] * 1.4426950408889634f : -CUDART_INF_F;
-          if (l != 0.f || sk != -CUDART_INF_F) {               // a NaN sum passes
-            const float top = fmaxf(l != 0.f ? m : -CUDART_INF_F, sk);
-            const float e = l != 0.f ? exp2f(m - top) : 0.f;
-            coef = l != 0.f ? e / (e * l + exp2f(sk - top)) : 0.f;
-          }
+      float* sx = s_x + (bc++ & 1) * 256;
+      sx[64 * (2 * half + cg) + r] = l;
+      named_bar_sync(1, kSoft);
+      l = (sx[r] + sx[64 + r]) + (sx[128 + r] + sx[192 + r]);
+      float coef = 0.f;
+      if (valid) {
+        const float sk = p.sink ? p.sink[r % p.H] * 1.4426950408889634f : -CUDART_INF_F;
+        if (l != 0.f || sk != -CUDART_INF_F) {               // a NaN sum passes
+          const float top = fmaxf(l != 0.f ? m : -CUDART_INF_F, sk);
+          const float f = l != 0.f ? exp2f(m - top) : 0.f;
+          coef = l != 0.f ? f / (f * l + exp2f(sk - top)) : 0.f;
         }
-        g += nt;
-        if (nt > 0) ok = ok && wait_warp(pv_done, (g - 1) & 1, abort_flag);
-        tc_fence_after();
-        // Rows [first, rows) of this CTA are tokens' results.
-        const int64_t orow = (w.tok0 + (int64_t)cta * w.tpc) * p.H;
-        const int rows = max(0, min(w.tpc, w.ntok - (int)cta * w.tpc)) * p.H;
-        const int first = (int)min((int64_t)rows, max((int64_t)0, -(w.pos0 + (int64_t)cta * w.tpc)) * p.H);
+      }
+      g += nt;
+      if (nt > 0) ok = ok && wait_warp(pv_done, (g - 1) & 1, abort_flag);
+      tc_fence_after();
+      // Rows [first, rows) of this CTA are tokens' results.
+      const int64_t orow = (w.tok0 + (int64_t)cta * w.tpc) * p.H;
+      const int rows = max(0, min(w.tpc, w.ntok - (int)cta * w.tpc)) * p.H;
+      const int first = (int)min((int64_t)rows, max((int64_t)0, -(w.pos0 + (int64_t)cta * w.tpc)) * p.H);
 #pragma unroll 1
-        for (int j = 0; j < 2; ++j) {
-          // columns 128 j + 32 c of O: dims 256 j + 128 half + 32 c.  A row of bf16
-          // goes through P's shared memory (P is done with), so that a warp writes 512
-          // bytes of one row at a time: rows written by their own threads took 4,000
-          // cycles an item more.
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            if (nt > 0 && ok) {
-              __syncwarp();
-              tmem_ld32(tmem + lane_base + 128 * j + 32 * c, o);
-              tmem_wait_ld();
-            } else {
+      for (int u = 0; u < 2; ++u) {
+        // columns 128 cg + 64 u .. of O: dims 256 cg + 128 half + 64 u ..  Rows of bf16
+        // go through P's shared memory (P is done with), so that a warp writes whole
+        // lines: rows written by their own threads took 4,000 cycles an item more.
+        float o[64];
+        if (nt > 0 && ok) {
+          __syncwarp();
+          tmem_ld32(tmem + lane_base + 128 * cg + 64 * u, o);
+          tmem_ld32(tmem + lane_base + 128 * cg + 64 * u + 32, o + 32);
+          tmem_wait_ld();
+        } else {
 #pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] = 0.f;
+          for (int q = 0; q < 64; ++q) o[q] = 0.f;
+        }
+        if (u == 1 && nt > 0) {                              // the next item may overwrite O
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader(o_free);
+        }
+#pragma unroll
+        for (int q = 0; q < 64; ++q) o[q] = coef == 0.f ? 0.f : o[q] * coef;
+        if (p.out_bf16) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_shared16(smem_u32(sP) + (2 * cg + half) * kSlab + swz128(r, q),
+                        make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
+                                   pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7])));
+          named_bar_sync(1, kSoft);
+          if (ok) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + orow * kD + 128 * (lane >> 3) + 64 * u + 8 * (lane & 7);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int rr = warp + 8 * q;
+              if (rr >= first && rr < rows)
+                *reinterpret_cast<uint4*>(out + (int64_t)rr * kD) =
+                    *reinterpret_cast<const uint4*>(sP + (lane >> 3) * kSlab + swz128(rr, lane & 7));
             }
-#pragma unroll
-            for (int q = 0; q < 32; ++q) o[q] = coef == 0.f ? 0.f : o[q] * coef;
-            if (p.out_bf16) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                st_shared16(smem_u32(sP) + (2 * half + (c >> 1)) * kSlab + swz128(r, 4 * (c & 1) + q),
-                            make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
-                                       pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7])));
-            } else if (valid && ok) {
-              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (orow + r) * kD + 256 * j + 128 * half + 32 * c);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-            }
           }
-          if (j == 1 && nt > 0) {                            // the next item may overwrite O
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_leader(o_free);
-          }
-          if (p.out_bf16) {
-            named_bar_sync(1, 128);
-            if (ok)
-              for (int rr = first + warp; rr < rows; rr += 4) {
-                const uint4 v = *reinterpret_cast<const uint4*>(sP + (lane >> 3) * kSlab + swz128(rr, lane & 7));
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (orow + rr) * kD + 256 * j + 8 * lane) = v;
-              }
-            if (j == 0) named_bar_sync(1, 128);
-          }
+          if (u == 0) named_bar_sync(1, kSoft);
+        } else if (valid && ok) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (orow + r) * kD + 256 * cg + 128 * half + 64 * u);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
     }
@@ -788,7 +777,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                            // neither CTA leaves while the other may reach it
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512));
   }
@@ -814,7 +803,7 @@ csa_status_t launch_paged_pair(PairParams& p, cudaStream_t st) {
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (pages) failed");
   }
-  const size_t smem = 1024 + 12 * kSlab + 2 * kStages * kStage + (5 * kStages + 9 + 2 * kItems) * 8 + 256 * 4 + 16;
+  const size_t smem = 12 * kSlab + 2 * kStages * kStage + (5 * kStages + 9 + 2 * kItems) * 8 + 512 * 4 + kItems * sizeof(Work) + 16;
   cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
   // Every sequence's last tile may be partly filled: an upper bound of the tiles
