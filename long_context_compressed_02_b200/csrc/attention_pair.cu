@@ -16,14 +16,13 @@
 // [0, N/2) in lanes 0-63 and [N/2, N) in lanes 64-127: O takes 256 columns, two
 // S buffers 128 each, all 512.
 //
-// K and V stream through a ring of two 32 KB stages each (8 MMAs a stage): K as
-// 128 rows x 128 dims, V as 64 rows x 256 dims.  Each has a producer and an
+// K and V stream through a ring of four 16 KB stages each (4 MMAs a stage): K as
+// 128 rows x 64 dims, V as 64 rows x 128 dims.  Each has a producer and an
 // issuer of its own (one thread cannot issue the copies of both, at about 100
-// cycles a copy).  PV(t) runs next to S(t + 2), and the softmax of tile t + 1
-// under both: it takes its logits out of TMEM at once and holds its probabilities
-// in registers until PV(t) is done with P.  Eight warps share it, two on each
-// scheduler, so that one's waits cover the other's (with four, a tile took 5,400
-// cycles and the tensor pipe waited for it).
+// cycles a copy).  S(t + 2) is issued behind PV(t), so that the tensor pipe has it
+// to do while the softmax of tile t + 1, which holds its probabilities in registers
+// until PV(t) is done with P, writes them.  Eight warps share the softmax, two on
+// each scheduler, so that one's waits cover the other's.
 //
 // Clusters are persistent and take every n-th pair of token groups (an item).
 // Tiles follow one another over the items, and one warp looks the items up ahead
@@ -62,9 +61,9 @@ namespace {
 constexpr int kD = 512;
 constexpr int kBlock = 64;                 // rows of a block: one page box, one slab of P
 constexpr int kTileBlocks = 4;             // 256 rows a tile
-constexpr int kStages = 2;                 // of each ring
-constexpr uint32_t kStage = 32768;         // K: [2 x 64 dims][128 rows], V: [4 x 64 dims][64 rows]
-constexpr int kKStages = 4;                // stages of a tile's K; its V has one for each block
+constexpr int kStages = 4;                 // of each ring
+constexpr uint32_t kStage = 16384;         // K: [128 rows][64 dims], V: [2 x 64 dims][64 rows]
+constexpr int kKStages = 8;                // stages of a tile's K; its V has two for each block
 constexpr uint32_t kSlab = 8192;           // 64 rows x 128 bytes
 // warps 0-7 softmax and output, 8 loads Q and K, 11 loads V, 9 issues S and 10 PV
 // (in CTA 0), 12 and 13 patch V blocks, 14 looks up items
@@ -146,8 +145,8 @@ __device__ __forceinline__ void tma_load_pair_4d(void* dst, const CUtensorMap* m
 }
 // MMAs and their commits are issued by whole warps in convergent code, with the
 // instruction itself predicated on one elected lane: descriptors then stay in
-// uniform registers, and a stage of 8 MMAs with its wait and its commit issues at
-// the tensor pipe's rate (64.9 cycles an MMA; from a branch that one lane takes,
+// uniform registers, and 8 MMAs with a wait and a commit issue at
+// the tensor pipe's rate (65 cycles an MMA; from a branch that one lane takes,
 // 84 in a bare loop and 97 to 130 in this kernel).
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
@@ -235,8 +234,8 @@ __device__ __forceinline__ bool block_clean(const Work& w, int kb) {
 
 // Tensor maps: the queries as [rows, 512], boxes of 64 x 64; each page store for
 // K as [rows, 512], boxes of (at most 64 rows of a page) x 64, and for V as
-// [2 of 256 dims][4 of 64][rows][64], boxes of 2 x 2 x rows x 64: a CTA's V block
-// is one copy.
+// [2 of 256 dims][4 of 64][rows][64], boxes of 1 x 2 x rows x 64: a V stage is one
+// copy.
 struct PairMaps {
   CUtensorMap q, k[2], v[2];
 };
@@ -321,7 +320,8 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
   uint64_t* s_free = s_full + 2;                             // [2] CTA 0: read by the softmax of both CTAs
   uint64_t* p_full = s_free + 2;                             // CTA 0: P and the rescaled O of both CTAs
   uint64_t* pv_done = p_full + 1;
-  float* s_x = reinterpret_cast<float*>(pv_done + 1);        // [2][4][64] maxima / sums of the row quarters
+  uint64_t* pv_sent = pv_done + 1;                           // CTA 0: the MMAs of a PV are issued
+  float* s_x = reinterpret_cast<float*>(pv_sent + 1);        // [2][4][64] maxima / sums of the row quarters
   Work* s_work = reinterpret_cast<Work*>(s_x + 512);         // [4]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_work + kItems);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
@@ -337,7 +337,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
     for (int i = 0; i < kItems; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_free[i], 14); }
     mbar_init(q_full, 2); mbar_init(q_free, 1); mbar_init(o_free, 16);
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 16); }
-    mbar_init(p_full, 16); mbar_init(pv_done, 1);
+    mbar_init(p_full, 16); mbar_init(pv_done, 1); mbar_init(pv_sent, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
@@ -448,14 +448,10 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
         ok = wait_warp(&empty_k[sl], ((st / kStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
         if (lane == 0) {
-          if (n) expect_leader(&full_k[sl], n * 2 * kSlab);
+          if (n) expect_leader(&full_k[sl], n * kSlab);
           else arrive_leader(&full_k[sl]);
         }
-        if (mine) {
-          uint8_t* dst = sK + sl * kStage + (kb & 1) * kSlab + j * t.rows * 128;
-          tma_load_pair(dst, map, 128 * d, t.y, &full_k[sl]);
-          tma_load_pair(dst + 2 * kSlab, map, 128 * d + 64, t.y, &full_k[sl]);
-        }
+        if (mine) tma_load_pair(sK + sl * kStage + (kb & 1) * kSlab + j * t.rows * 128, map, 64 * d, t.y, &full_k[sl]);
       }
     }
   } else if (warp == 11) {
@@ -468,26 +464,26 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       const Part t = part_of(x);
       const CUtensorMap* map = t.s ? &maps.v[1] : &maps.v[0];
       const CUtensorMap* part = t.s ? &maps.k[1] : &maps.k[0];
-      const int nbk = blocks_of(x.w, x.i);
-      for (int v = 0; v < nbk; ++v, ++st) {
+      const int nv = 2 * blocks_of(x.w, x.i);
+      for (int v = 0; v < nv; ++v, ++st) {                   // dims 256 (v & 1) + 128 cta .. of block v / 2
         const uint32_t sl = st % kStages;
         ok = wait_warp(&empty_v[sl], ((st / kStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
-        const bool clean = block_clean(x.w, kTileBlocks * x.i + v);
+        const bool clean = block_clean(x.w, kTileBlocks * x.i + (v >> 1));
         if (lane == 0) {
           if (clean) expect_leader(&full_v[sl], kStage);
           else mbar_expect_tx(&patch[sl], kStage);
         }
-        if (t.on && kb == v) {
-          // the block's rows lie in all four slabs: one copy, or one for each part and slab
+        if (t.on && kb == (v >> 1)) {
+          // the block's rows lie in both slabs: one copy, or one for each part and slab
           uint8_t* dst = sV + sl * kStage + j * t.rows * 128;
           if (t.rows == kBlock) {
-            if (clean) tma_load_pair_4d(dst, map, 0, t.y, 2 * (int)cta, 0, &full_v[sl]);
-            else tma_load_4d(dst, map, 0, t.y, 2 * (int)cta, 0, &patch[sl]);
+            if (clean) tma_load_pair_4d(dst, map, 0, t.y, 2 * (int)cta, v & 1, &full_v[sl]);
+            else tma_load_4d(dst, map, 0, t.y, 2 * (int)cta, v & 1, &patch[sl]);
           } else {
-#pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
-              const int d = 256 * (h >> 1) + 128 * (int)cta + 64 * (h & 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int d = 256 * (v & 1) + 128 * (int)cta + 64 * h;
               if (clean) tma_load_pair(dst + h * kSlab, part, d, t.y, &full_v[sl]);
               else tma_load_2d(dst + h * kSlab, part, d, t.y, &patch[sl]);
             }
@@ -503,10 +499,11 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
     Stream x;
     while (ok && advance(x, 2, 64)) {
       const int nbk = blocks_of(x.w, x.i);
-      for (int kb = 0; kb < nbk; ++kb, ++st) {
-        if (block_clean(x.w, kTileBlocks * x.i + kb)) continue;
+      for (int v = 0; v < 2 * nbk; ++v, ++st) {
+        const int kb = kTileBlocks * x.i + (v >> 1);
+        if (block_clean(x.w, kb)) continue;
         int row;
-        const int s = block_at(x.w, kTileBlocks * x.i + kb, row);
+        const int s = block_at(x.w, kb, row);
         row += lt;
         const bool any = row >= (s ? x.w.any_lo[1] : x.w.any_lo[0]) && row < (s ? x.w.any_hi[1] : x.w.any_hi[0]);
         const bool all = row >= (s ? x.w.all_lo[1] : x.w.all_lo[0]) && row < (s ? x.w.all_hi[1] : x.w.all_hi[0]);
@@ -517,14 +514,14 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
         if (!ok) break;
         if (!all) {
 #pragma unroll 4
-          for (int q = 0; q < 32; ++q) {                     // the row's 32 pieces of 16 bytes
+          for (int q = 0; q < 16; ++q) {                     // the row's 16 pieces of 16 bytes
             uint8_t* at = sV + sl * kStage + (q >> 3) * kSlab + swz128(lt, (q + lt) & 7);
-            uint4 v = make_uint4(0, 0, 0, 0);
+            uint4 z = make_uint4(0, 0, 0, 0);
             if (any) {
-              v = *reinterpret_cast<const uint4*>(at);
-              v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+              z = *reinterpret_cast<const uint4*>(at);
+              z = make_uint4(finite2(z.x), finite2(z.y), finite2(z.z), finite2(z.w));
             }
-            st_shared16(smem_u32(at), v);
+            st_shared16(smem_u32(at), z);
           }
         }
         fence_proxy_async_smem();
@@ -542,6 +539,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
     Stream x;
     for (; advance(x, 0, 0); ++t) {
       if (ok && x.i == 0) ok = wait_warp(q_full, (x.items & 1) ^ 1, abort_flag);
+      ok = ok && (t < 2 || wait_warp(pv_sent, t & 1, abort_flag));       // behind PV(t - 2)
       ok = ok && wait_warp(&s_free[t & 1], ((t >> 1) & 1) ^ 1, abort_flag);
       if (!ok) continue;
       for (int d = 0; d < kKStages; ++d, ++st) {
@@ -550,9 +548,9 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int m = 0; m < 8; ++m)
-          mma_pair(tmem + kSCol + 128 * (t & 1), dQ + (((2 * d + (m >> 2)) * kSlab + (m & 3) * 32) >> 4),
-                   dK + ((sl * kStage + (m >> 2) * 2 * kSlab + (m & 3) * 32) >> 4), idesc, (d | m) != 0);
+        for (int m = 0; m < 4; ++m)
+          mma_pair(tmem + kSCol + 128 * (t & 1), dQ + ((d * kSlab + m * 32) >> 4), dK + ((sl * kStage + m * 32) >> 4), idesc,
+                   (d | m) != 0);
         commit_pair(&empty_k[sl]);
       }
       if (ok) {
@@ -573,18 +571,19 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       if (ok && x.i == 0) ok = wait_warp(o_free, x.items & 1, abort_flag);
       ok = ok && wait_warp(p_full, t & 1, abort_flag);
       if (!ok) continue;
-      const int nbk = blocks_of(x.w, x.i);
-      for (int kb = 0; kb < nbk; ++kb, ++st) {
+      const int nv = 2 * blocks_of(x.w, x.i);
+      for (int v = 0; v < nv; ++v, ++st) {
         const uint32_t sl = st % kStages;
         ok = wait_warp(&full_v[sl], (st / kStages) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int m = 0; m < 8; ++m)
-          mma_pair(tmem + 128 * (m >> 2), dP + ((kb * kSlab + (m & 3) * 32) >> 4),
-                   dV + ((sl * kStage + (m >> 2) * 2 * kSlab + (m & 3) * 2048) >> 4), idesc, (x.i | kb | (m & 3)) != 0);
+        for (int m = 0; m < 4; ++m)
+          mma_pair(tmem + 128 * (v & 1), dP + (((v >> 1) * kSlab + m * 32) >> 4), dV + ((sl * kStage + m * 2048) >> 4), idesc,
+                   (x.i | (v >> 1) | m) != 0);
         commit_pair(&empty_v[sl]);
       }
+      if (lane == 0) mbar_arrive(pv_sent);
       if (ok) commit_pair(pv_done);
     }
   } else {
@@ -612,63 +611,84 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
         const uint32_t t = g + i;
         // the columns of the block that the row's token sees: [a, e)
         const int kb = kTileBlocks * i + 2 * half + cg;
-        int a = 0, e = 0;
-        if (kb < w.nb) {
-          int row;
-          const int s = block_at(w, kb, row);
-          a = (s ? lo[1] : lo[0]) - row;
-          e = (s ? hi[1] : hi[0]) - row;
+        const bool whole = kb < w.nb && block_clean(w, kb);
+        int a = 0, e = kBlock;
+        if (!whole) {
+          e = 0;
+          if (kb < w.nb) {
+            int row;
+            const int s = block_at(w, kb, row);
+            a = (s ? lo[1] : lo[0]) - row;
+            e = (s ? hi[1] : hi[0]) - row;
+          }
         }
-        const bool whole = __all_sync(0xffffffffu, a <= 0 && e >= kBlock);
         ok = ok && wait_warp(&s_full[t & 1], (t >> 1) & 1, abort_flag);
+        tc_fence_after();
+        const uint32_t ts = tmem + lane_base + kSCol + 128 * (t & 1) + 64 * cg;
+        // This row's logits, those that its token does not see as -inf.  A visible
+        // logit of -inf is a non-finite row's, whose V may read as zeros.
         float x[64];
-        if (ok) {
-          tc_fence_after();
-          const uint32_t ts = tmem + lane_base + kSCol + 128 * (t & 1) + 64 * cg;
+        bool nan = false;
+        auto logits = [&]() {
           tmem_ld32(ts, x);
           tmem_ld32(ts + 32, x + 32);
           tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_leader(&s_free[t & 1]);
-        }
-        bool nan = false;
-        if (!whole) {
-          // a visible logit of -inf is a non-finite row's, whose V may read as zeros
+          if (!(whole && valid)) {
 #pragma unroll
-          for (int q = 0; q < 64; ++q) {
-            const bool on = q >= a && q < e;
-            nan |= on && x[q] == -CUDART_INF_F;
-            x[q] = on ? x[q] : -CUDART_INF_F;
+            for (int q = 0; q < 64; ++q) {
+              const bool on = q >= a && q < e && valid;
+              nan |= on && x[q] == -CUDART_INF_F;
+              x[q] = on ? x[q] : -CUDART_INF_F;
+            }
           }
-        }
-        float m4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int q = 4; q < 64; ++q) m4[q & 3] = fmaxf(m4[q & 3], x[q]);
-        float* sx = s_x + (bc++ & 1) * 256;
-        sx[64 * (2 * half + cg) + r] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        if (named_bar_or(1, kSoft, !ok)) ok = false;
-        if (!ok) continue;
-        const float mx = fmaxf(fmaxf(sx[r], sx[64 + r]), fmaxf(sx[128 + r], sx[192 + r])) * p.scale_log2;
-        // The maximum moves only when it grows by more than 2^kTau.
-        float alpha = 1.f;
-        if (mx > m + kTau) {
-          alpha = exp2f(m - mx);                             // 0 the first time
-          m = mx;
-        }
-        l *= alpha;
-        const float ref = nan ? CUDART_NAN_F : m == -CUDART_INF_F ? 0.f : m;
-        // probabilities, as bf16 pairs in registers
+          __syncwarp();
+        };
+        // probabilities against the maximum m, as bf16 pairs in registers
         uint32_t pk[32];
-        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float sum = 0.f;
+        auto weights = [&]() {
+          const float ref = nan ? CUDART_NAN_F : m == -CUDART_INF_F ? 0.f : m;
+          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          const float2 z = fma2(make_float2(x[2 * q], x[2 * q + 1]), make_float2(p.scale_log2, p.scale_log2), make_float2(-ref, -ref));
-          const float2 y = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-          l2[q & 1] = add2(l2[q & 1], y);
-          pk[q] = pack2(y.x, y.y);
+          for (int q = 0; q < 32; ++q) {
+            const float2 z = fma2(make_float2(x[2 * q], x[2 * q + 1]), make_float2(p.scale_log2, p.scale_log2), make_float2(-ref, -ref));
+            const float2 y = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+            l2[q & 1] = add2(l2[q & 1], y);
+            pk[q] = pack2(y.x, y.y);
+          }
+          sum = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+        };
+        // The maximum moves only when it grows by more than 2^kTau, which is rare past
+        // the first tiles: the weights are formed against the old one while the four
+        // threads of the rows find out, and formed again if it must move.
+        float mx = -CUDART_INF_F;
+        if (ok) {
+          logits();
+          float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int q = 4; q < 64; ++q) m4[q & 3] = fmaxf(m4[q & 3], x[q]);
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          weights();
         }
-        l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+        float alpha = 1.f;
+        if (named_bar_or(1, kSoft, !ok || mx * p.scale_log2 > m + kTau)) {
+          float* sx = s_x + (bc++ & 1) * 256;
+          sx[64 * (2 * half + cg) + r] = mx;
+          if (named_bar_or(1, kSoft, !ok)) ok = false;
+          if (!ok) continue;
+          mx = fmaxf(fmaxf(sx[r], sx[64 + r]), fmaxf(sx[128 + r], sx[192 + r])) * p.scale_log2;
+          if (mx > m + kTau) {
+            alpha = exp2f(m - mx);                           // 0 the first time
+            m = mx;
+          }
+          __syncwarp();
+          logits();
+          weights();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(&s_free[t & 1]);
+        l = l * alpha + sum;
         // P and O are free once PV(t - 1) is done (of an earlier item: its epilogue waited)
         if (i > 0) {
           ok = wait_warp(pv_done, (t - 1) & 1, abort_flag);
@@ -796,14 +816,14 @@ csa_status_t launch_paged_pair(PairParams& p, cudaStream_t st) {
     const cuuint64_t rows = (cuuint64_t)p.pt[s].n_pages * ps;
     const cuuint32_t box_rows = (cuuint32_t)std::min(ps, kBlock);
     const cuuint64_t dims[4] = {64, rows, 4, 2}, strides[3] = {kD * 2, 128, 512};
-    const cuuint32_t box[4] = {64, box_rows, 2, 2}, step[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, box_rows, 2, 1}, step[4] = {1, 1, 1, 1};
     if (!encode_2d(&maps.k[s], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.rows[s], kD, rows, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
         tmap_encoder()(&maps.v[s], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.rows[s]), dims, strides, box, step,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (pages) failed");
   }
-  const size_t smem = 12 * kSlab + 2 * kStages * kStage + (5 * kStages + 9 + 2 * kItems) * 8 + 512 * 4 + kItems * sizeof(Work) + 16;
+  const size_t smem = 12 * kSlab + 2 * kStages * kStage + (5 * kStages + 10 + 2 * kItems) * 8 + 512 * 4 + kItems * sizeof(Work) + 16;
   cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
   // Every sequence's last tile may be partly filled: an upper bound of the tiles
