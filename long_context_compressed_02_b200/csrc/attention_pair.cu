@@ -515,7 +515,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
         if (!all) {
 #pragma unroll 4
           for (int q = 0; q < 16; ++q) {                     // the row's 16 pieces of 16 bytes
-            uint8_t* at = sV + sl * kStage + (q >> 3) * kSlab + swz128(lt, (q + lt) & 7);
+            uint8_t* at = sV + sl * kStage + (q >> 3) * kSlab + swz128(lt, q & 7);
             uint4 z = make_uint4(0, 0, 0, 0);
             if (any) {
               z = *reinterpret_cast<const uint4*>(at);
@@ -593,6 +593,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
     // block 2 half + cg, cg = w / 4.
     const int r = tid & 63, half = (warp >> 1) & 1, cg = warp >> 2;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const float sk = p.sink ? p.sink[r % p.H] * 1.4426950408889634f : -CUDART_INF_F;
     uint32_t g = 0, bc = 0;                                  // tiles and exchanges of the items before
     bool ok = true;
     Work w;
@@ -725,7 +726,6 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       l = (sx[r] + sx[64 + r]) + (sx[128 + r] + sx[192 + r]);
       float coef = 0.f;
       if (valid) {
-        const float sk = p.sink ? p.sink[r % p.H] * 1.4426950408889634f : -CUDART_INF_F;
         if (l != 0.f || sk != -CUDART_INF_F) {               // a NaN sum passes
           const float top = fmaxf(l != 0.f ? m : -CUDART_INF_F, sk);
           const float f = l != 0.f ? exp2f(m - top) : 0.f;
