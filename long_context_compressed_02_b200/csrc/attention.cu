@@ -925,6 +925,20 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     // shape, so one thread cannot keep the tensor pipe fed with these small
     // products: warp 8 issues the even slabs of S, warp 10 the odd slabs (the
     // two accumulators of h's S buffer, side by side), warp 9 the PV products.
+    // Paged calls issue from whole warps, the instruction alone predicated on one
+    // elected lane: in convergent code the descriptors stay in uniform registers.
+    auto wait_issuer = [&](uint64_t* bar, uint32_t parity) {
+      const bool r = wait_bar(bar, parity, abort_flag);
+      return PAGED ? __all_sync(0xffffffffu, r) != 0 : r;
+    };
+    auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+      if constexpr (PAGED) mma_bf16_elect(d, da, db, idesc, acc);
+      else mma_bf16(d, da, db, idesc, acc);
+    };
+    auto commit = [&](uint64_t* bar) {
+      if constexpr (PAGED) mma_commit_elect(bar);
+      else mma_commit(bar);
+    };
     const int role = warp - 8;                 // 0: S even slabs, 1: PV, 2: S odd slabs
     const uint32_t idesc_s = make_idesc(64, kNQ, 1, 1, 0, 0);
     const uint32_t idesc_o = make_idesc(128, kNQ, 1, 1, 1, 1);
@@ -940,10 +954,10 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     // accumulators; each pair commits its two tiles' barriers, which free their
     // slabs for the next loads.
     auto issue_pv = [&](uint32_t h, bool first) -> bool {
-      if (!wait_bar(&p_full[h & 1], (h >> 1) & 1, abort_flag)) return false;
+      if (!wait_issuer(&p_full[h & 1], (h >> 1) & 1)) return false;
       if (first) {
         // O^T is overwritten: the previous item's epilogue must have read it
-        if (!wait_bar(epi_done, (pv_items & 1) ^ 1, abort_flag)) return false;
+        if (!wait_issuer(epi_done, (pv_items & 1) ^ 1)) return false;
         ++pv_items;
       }
       tc_fence_after();
@@ -957,12 +971,12 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           for (int j = 0; j < 2; ++j) {
             if (j < np) {
               const int tt = t0 + j;
-              mma_bf16(tmem + kOCol + 64 * tt, dO_A + ((slot * kSlot + 2 * tt * kSlab + kk * 2048) >> 4),
+              mma(tmem + kOCol + 64 * tt, dO_A + ((slot * kSlot + 2 * tt * kSlab + kk * 2048) >> 4),
                        dO_B + ((slot * kPBuf + kk * 2048) >> 4), idesc_o, (kk > 0 || !first) ? 1u : 0u);
             }
           }
         }
-        for (int j = 0; j < np; ++j) mma_commit(&pv_done[slot * NT + t0 + j]);
+        for (int j = 0; j < np; ++j) commit(&pv_done[slot * NT + t0 + j]);
       }
       return true;
     };
@@ -974,31 +988,31 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       const int b = it.b, t = it.t;
       const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per);
       if (rs.c1 <= rs.c0) continue;
-      if (lane == 0) {
+      if (PAGED || lane == 0) {
         if (role == 1) {
           for (int c = rs.c0; c < rs.c1 && ok; ++c, ++g)
             if (!issue_pv(g, c == rs.c0)) ok = false;
         } else {
-          if (!wait_bar(q_full, qcount & 1, abort_flag)) ok = false;
+          if (!wait_issuer(q_full, qcount & 1)) ok = false;
           ++qcount;
           const int hh = role == 0 ? 0 : 1;    // this issuer's slabs: 2 tt + hh
           for (int c = rs.c0; c < rs.c1 && ok; ++c, ++g) {
             const uint32_t slot = g & 1;
-            if (!wait_bar(&s_free[slot], ((g >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+            if (!wait_issuer(&s_free[slot], ((g >> 1) & 1) ^ 1)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
             for (int tt = 0; tt < NT; ++tt) {
-              if (!wait_bar(&kv_full[slot * NT + tt], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+              if (!wait_issuer(&kv_full[slot * NT + tt], (g >> 1) & 1)) { ok = false; break; }
               tc_fence_after();
               const int s = 2 * tt + hh;
 #pragma unroll
               for (int kq = 0; kq < 4; ++kq)
-                mma_bf16(tmem + 64 * slot + 128 * hh, dS_A + ((slot * kSlot + s * kSlab + kq * 32) >> 4),
+                mma(tmem + 64 * slot + 128 * hh, dS_A + ((slot * kSlot + s * kSlab + kq * 32) >> 4),
                          dS_B + ((s * kQSlab + kq * 32) >> 4), idesc_s, (tt | kq) != 0);
             }
             if (!ok) break;
-            mma_commit(&s_full[slot]);
-            if (c == rs.c1 - 1) mma_commit(q_free);
+            commit(&s_full[slot]);
+            if (c == rs.c1 - 1) commit(q_free);
           }
         }
       }
