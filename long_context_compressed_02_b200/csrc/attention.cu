@@ -546,6 +546,8 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         // are zero-filled, and their columns are never written out)
         if (lt == 0) {
           mbar_expect_tx(q_full, kNQ * D * 2);
+          if constexpr (PAGED) tma_load_3d(sQ, &map_q, 0, (int32_t)(bt * p.H), 0, q_full);   // all slabs in one copy
+          else
 #pragma unroll 1
           for (int s = 0; s < NS; ++s)
             tma_load_2d(sQ + s * kQSlab, &map_q, 64 * s, (int32_t)(bt * p.H), q_full);
@@ -586,9 +588,9 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       int pre_c = -1;                    // half chunk whose gathered row index pre_row holds
       int32_t pre_row = 0;
       // Paged rows: bulk prefetch of a half chunk into L2, page by page.  The ring
-      // holds two half chunks, too few to cover the latency of HBM; kAhead half
+      // holds two half chunks, too few to cover the latency of HBM; kAhead + 1 half
       // chunks ahead the loads find their rows in L2.
-      constexpr int kAhead = kCodes ? 4 : 3;
+      constexpr int kAhead = kCodes ? 4 : 1;
       auto prefetch = [&](int cc) {
         if (cc >= rs.c1) return;
         const bool w = cc < rs.nh2;
@@ -611,11 +613,26 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           }
         }
       };
-      if (PAGED && grp == 0 && lw == 0)
+      if (kCodes && grp == 0 && lw == 0)
         for (int i = 1; i <= kAhead; ++i) prefetch(rs.c0 + i);
+      // The row of the page store where a half chunk starts, looked up one ahead
+      // of its use (a load's latency that the copies would wait for).
+      auto start_of = [&](int cc) -> int64_t {
+        if (cc >= rs.c1) return -1;
+        const bool w = cc < rs.nh2;
+        return page_row(w ? p.pt2 : p.pt1, b, (w ? rs.lo2 : 0) + (int64_t)(w ? cc : cc - rs.nh2) * kRows);
+      };
+      int64_t start = PAGED ? start_of(rs.c0 + (kCodes && (int)(g & 1) != grp ? 1 : 0)) : 0;
       for (int c = rs.c0; c < rs.c1 && ok; ++c, ++g) {
         if (kCodes && (int)(g & 1) != grp) continue;
-        if (PAGED && lw == 0) prefetch(c + kAhead + 1);
+        const int64_t g0 = start;
+        if (PAGED) start = start_of(c + (kCodes ? 2 : 1));
+        // bf16: the second warp prefetches, so that the first's copies go out at once
+        if (PAGED && lw == (kCodes ? 0 : 1)) {
+          if (c == rs.c0 && !kCodes)
+            for (int i = 1; i <= kAhead; ++i) prefetch(rs.c0 + i);
+          prefetch(c + kAhead + 1);
+        }
         const int slot = g & 1;
         const uint32_t fpar = ((g >> 1) & 1) ^ 1;     // completion of PV(g - 2), which read this slot
         uint8_t* sl_base = sKV + slot * kSlot;
@@ -637,11 +654,8 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         if constexpr (PAGED) {
           const int64_t r0 = (win ? rs.lo2 : 0) + (int64_t)cl * kRows;
           tma = fullh && (r0 & (kRows - 1)) == 0 && (win ? p.tma_tok != 0 : p.tma_kv != 0);
-          if (tma) {
-            const int64_t g0 = page_row(win ? p.pt2 : p.pt1, b, r0);
-            tma = g0 >= 0;
-            y0 = (int32_t)g0;
-          }
+          tma = tma && g0 >= 0;
+          y0 = (int32_t)g0;
         } else {
           tma = win ? (p.tma_tok != 0 && (p.src2 == SRC2_WINDOW || fullh))
                     : (rs.idx == nullptr && p.tma_kv != 0 && fullh);
@@ -653,8 +667,12 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
             if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
             if (lt == 0) {
               mbar_expect_tx(&full[tt], 2 * kSlab);
+              if constexpr (PAGED) {
+                tma_load_3d(sl_base + (2 * tt) * kSlab, win ? &map_tok : &map_kv, 0, y0, 2 * tt, &full[tt]);
+              } else {
               tma_load_2d(sl_base + (2 * tt) * kSlab, win ? &map_tok : &map_kv, 128 * tt, y0, &full[tt]);
               tma_load_2d(sl_base + (2 * tt + 1) * kSlab, win ? &map_tok : &map_kv, 128 * tt + 64, y0, &full[tt]);
+              }
             } else {
               mbar_arrive(&full[tt]);
             }
@@ -2021,9 +2039,17 @@ extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H,
   p.scale = scale; p.scale_log2 = scale * 1.4426950408889634f;
   p.sink = sink; p.out = out; p.out_bf16 = out_dtype == CSA_BF16;
   p.max_items = paged_items(n_tok, n_seq);
-  // Chunks of several tokens a sequence share their rows on pairs of SMs.
+  // Chunks of several tokens a sequence share their rows on pairs of SMs, two of
+  // 64 heads or more of fewer (group).  A pair's turn costs more than a token's here
+  // (3,300 tokens of 64 heads, window 128: 376 us against 211) and a row less
+  // (window 1024: 674 against 926); they meet at 512 rows a token (506 and 505), or
+  // fewer with more tokens to share them (16 heads, window 128: 110 against 203).
+  // How many rows the tokens see is known on the device only, so the rule goes by
+  // the most that the window and the tables allow.
   const int64_t lim = (int64_t)1 << 31;
-  if (p.max_items == 0 && D == 512 && n_tok >= 2 * (int64_t)n_seq && kv_dtype == CSA_BF16 &&
+  const int64_t group = std::max(1, 64 / H);
+  const int64_t most = (tok_pages ? (W == 0 ? p.cap2 : std::min<int64_t>(W, p.cap2)) : 0) + (kv_pages ? p.cap : 0);
+  if (p.max_items == 0 && D == 512 && n_tok >= 2 * (int64_t)n_seq && kv_dtype == CSA_BF16 && most * group >= 512 &&
       (!tok_pages || (pair_page_size(tok_page_size) && n_tok_pages * tok_page_size < lim)) &&
       (!kv_pages || (pair_page_size(kv_page_size) && n_kv_pages * kv_page_size < lim))) {
     PairParams g{};
@@ -2035,17 +2061,17 @@ extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H,
   }
   AttnMaps maps;
   memset(&maps, 0, sizeof(maps));
-  if (!encode_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, D, n_tok * H, 64, kNQ, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!encode_slabs(&maps.q, q, D, n_tok * H, kNQ, D / 64))
     return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (queries) failed");
   p.tma_q = 1;
   // blocks of 64 rows lie within one page from 64 rows a page on
   if (p.src1 == SRC1_DENSE && kv_dtype == CSA_BF16 && kv_page_size >= kRows && n_kv_pages * kv_page_size < (int64_t)1 << 31) {
-    if (!encode_2d(&maps.kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_pages, D, n_kv_pages * kv_page_size, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_slabs(&maps.kv, kv_pages, D, n_kv_pages * kv_page_size, kRows, 2))
       return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (entries) failed");
     p.tma_kv = 1;
   }
   if (p.src2 == SRC2_WINDOW && tok_page_size >= kRows && n_tok_pages * tok_page_size < (int64_t)1 << 31) {
-    if (!encode_2d(&maps.tok, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, tok_pages, D, n_tok_pages * tok_page_size, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_slabs(&maps.tok, tok_pages, D, n_tok_pages * tok_page_size, kRows, 2))
       return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (tokens) failed");
     p.tma_tok = 1;
   }

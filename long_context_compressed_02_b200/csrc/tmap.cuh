@@ -34,4 +34,19 @@ inline bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t elem
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same rows as [inner / 64 slabs][rows][64], boxes of `box_slabs` slabs of
+// box_rows x 64: one copy fills consecutive 128-byte-swizzled slabs (bf16).
+inline bool encode_slabs(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
+                         uint32_t box_slabs) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t gdim[3] = {64, rows, inner / 64};
+  cuuint64_t gstride[2] = {inner * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, box_slabs};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace csa
