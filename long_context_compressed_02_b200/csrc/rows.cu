@@ -191,9 +191,11 @@ rows_kernel(const __grid_constant__ RowsParams p) {
 
   // Row lr of the task: token tok0 + lr / nr, head h0 + lr % nr.  K row groups
   // are in flight: a group's registers are refilled as soon as it is unpacked.
-  // lr / nr by a product: lr < 1024 and nr <= 128 where a task has several tokens
-  const uint32_t rcp = nt == 1 ? 0 : (65535u + nr) / nr;
-  auto token_of = [&](int lr) { return (int)(((uint32_t)lr * rcp) >> 16); };
+  // lr / nr by a product: the task's lr and the K groups ahead stay below 1024, and
+  // nr at most 256 where a task has several tokens, so rcp is less than 256 2^-20 / nr
+  // too large and lr times that does not reach the next 1 / nr
+  const uint32_t rcp = nt == 1 ? 0 : ((1u << 20) - 1 + nr) / nr;
+  auto token_of = [&](int lr) { return (int)(((uint32_t)lr * rcp) >> 20); };
   uint4 raw[K][UPL][2][NV];
   auto load_row = [&](int k, int lr) {
     if (lr >= total) return;

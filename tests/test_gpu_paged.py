@@ -112,6 +112,23 @@ def test_rope_views_other_dtype_and_autograd_identity(csa):
     assert abs(a - b) <= SLOP * float(np.abs(np64(g) * np64(y)).sum())
 
 
+@pytest.mark.parametrize("H", [129, 200, 255, 256])
+def test_rope_of_many_narrow_heads(csa, H):
+    """A warp's task holds several tokens of more than 128 heads."""
+    cu, qp, n, _ = batch([2500, 2500], [7, 100])
+    x = torch.randn(n, H, 16, device="cuda").to(BF)
+    w, _ = csa.csa_rope_freqs(16)
+    out = csa.csa_rope(x, cu, qp, w)
+    pos = torch.cat([torch.arange(2500) + 7, torch.arange(2500) + 100]).double().cuda()
+    a = (pos[:, None] * w)[:, None]
+    X = x.double()
+    ref = torch.cat([X[..., :8] * a.cos() - X[..., 8:] * a.sin(), X[..., :8] * a.sin() + X[..., 8:] * a.cos()], -1)
+    tol = half(BF) * ref.abs() + SLOP * 2 * X.abs().amax(-1, keepdim=True)
+    assert bool(((out.double() - ref).abs() <= tol).all())
+    same = x.clone()
+    assert torch.equal(csa.csa_rope(same, cu, qp, w, out=same), out)
+
+
 # ---------------------------------------------------------------- queries and keys
 
 @pytest.mark.parametrize("name", BATCHES)
