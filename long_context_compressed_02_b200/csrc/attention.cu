@@ -188,18 +188,22 @@ __device__ __forceinline__ RowSet row_set_warp(const AttnParams& p, int b, int t
   return r;
 }
 
-// Half chunks of the row set of a paged call's query at position pos.
-__device__ __forceinline__ int paged_half_chunks(const AttnParams& p, int64_t pos) {
+// The most half chunks of a row set of a paged call's queries at positions
+// pos0 .. pos1: the entries grow with the position, the window until its end
+// reaches the end of the table.
+__device__ __forceinline__ int paged_half_chunks(const AttnParams& p, int64_t pos0, int64_t pos1) {
   int64_t n1 = 0, n2 = 0;
-  if (p.src1 == SRC1_DENSE) n1 = max((int64_t)0, min(p.cap, (pos + 1) / p.m));
-  if (p.src2 == SRC2_WINDOW)
+  if (p.src1 == SRC1_DENSE) n1 = max((int64_t)0, min(p.cap, (pos1 + 1) / p.m));
+  if (p.src2 == SRC2_WINDOW) {
+    const int64_t pos = max(pos0, min(pos1, p.cap2 - 1));
     n2 = max((int64_t)0, min(p.cap2, pos + 1) - (p.W == 0 ? 0 : max((int64_t)0, pos - p.W + 1)));
+  }
   return (int)((n1 + kRows - 1) / kRows + (n2 + kRows - 1) / kRows);
 }
 
 // Work items of a paged call with few query tokens.  Every row set is cut into
 // ranges of `per` half chunks; sequence b's tokens take ranges first[b] ..
-// first[b + 1] - 1, the same number each (that of its last token).  `per` is
+// first[b + 1] - 1, the same number each (that of its longest row set).  `per` is
 // the smallest step of the search below that leaves at most max_items ranges,
 // one for each SM, so that the call is one wave whatever the lengths are: they
 // are known on the device only.  Without empty ranges to step over, an item
@@ -207,14 +211,14 @@ __device__ __forceinline__ int paged_half_chunks(const AttnParams& p, int64_t po
 constexpr int kPlanSeqs = 1024;    // sequences that the shared-memory plan holds
 struct SplitPlan {
   int32_t first[kPlanSeqs + 1];
-  int32_t nh[kPlanSeqs];           // half chunks of the sequence's last token
+  int32_t nh[kPlanSeqs];           // half chunks of the sequence's longest row set
   int per;
 };
 __device__ __forceinline__ void make_plan(const AttnParams& p, SplitPlan& s, int tid, int nthreads) {
   for (int b = tid; b < p.n_seq; b += nthreads) {
     const int len = p.cu_q[b + 1] - p.cu_q[b];
     // a token without rows still has one (empty) range, which tells the merge so
-    s.nh[b] = len > 0 ? max(1, paged_half_chunks(p, p.q_pos[b] + len - 1)) : 0;
+    s.nh[b] = len > 0 ? max(1, paged_half_chunks(p, p.q_pos[b], p.q_pos[b] + len - 1)) : 0;
     s.first[b] = max(0, len);      // the lengths, until the prefix sums replace them
   }
   __syncthreads();

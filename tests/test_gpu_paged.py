@@ -465,6 +465,20 @@ def test_rows_behind_the_table_are_not_visible(csa):
     assert torch.equal(short, ref)
 
 
+@pytest.mark.parametrize("lens,pos,H,D,W,cut", [([20], [250], 64, 512, 128, 256), ([20], [250], 8, 128, 128, 256),
+                                                 ([20, 1], [200, 400], 64, 512, 0, 192), ([100], [1000], 64, 512, 600, 1024),
+                                                 ([100], [250], 8, 128, 128, 256)])
+def test_tokens_behind_the_table(csa, lens, pos, H, D, W, cut):
+    """A window that reaches over the table's end shrinks from token to token."""
+    c = Case(lens=lens, pos=pos, H=H, D=D, W=W)
+    out = csa.csa_paged_attention(c.q, c.cu, c.qp, **dict(c.kw, tok_table=c.kw["tok_table"][:, :cut // 64].contiguous()))
+    csa.check_device_error()
+    for i, b, p in c.toks[::3]:
+        rows = O.page_rows(np64(c.pages), c.tab[b], 0 if W == 0 else max(0, p - W + 1), min(p + 1, cut))
+        ref, mag = O.paged_attention_row(np64(c.q[i]), rows, 1 / math.sqrt(D), np64(c.sink))
+        assert np.all(np.abs(np64(out[i]) - ref) <= (2.0 ** -8 + 2.0 ** -9) * mag + half(BF) * np.abs(ref)), (i, p)
+
+
 def test_offsets_beyond_32_bits(csa):
     """Pages behind 2^32 elements of a large cache."""
     ps, D, n_pages = 64, 512, 140000                          # 9.2 GB, 4.6e9 elements
