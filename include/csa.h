@@ -399,7 +399,8 @@ csa_status_t csa_grouped_out_proj(const void* o, const void* w_grp, const void* 
  *     cu_q[b] .. cu_q[b+1] - 1 (none is allowed), at positions q_pos[b],
  *     q_pos[b] + 1, ... (q_pos [n_seq] int64).  Both are DEVICE arrays.  Rows
  *     behind cu_q[n_seq] (a padded batch) and rows at negative positions are
- *     left as they were: their outputs are not written.
+ *     left as they were: their outputs are not written.  cu_q[n_seq] may be
+ *     above n_tok: only rows below n_tok are touched.
  *   Pages: a cache is [n_pages, page_size, row] with page_size a power of two;
  *     row p of sequence b is row p % page_size of page
  *     block_table[b * max_pages + p / page_size] (int32, DEVICE).  Entries of
@@ -482,7 +483,10 @@ csa_status_t csa_paged_append(const void* rows, csa_dtype_t in_dtype, int64_t ro
  *   scale > 0.
  *   tok_pages [n_tok_pages, tok_page_size, D] BF16.
  *   kv_pages [n_kv_pages, kv_page_size, D] BF16, or E4M3 with kv_rope and
- *     kv_scale (the row format of csa_paged_append).
+ *     kv_scale (the row format of csa_paged_append).  E4M3 rows enter the
+ *     products as their codes, which bf16 holds exactly, and their last 64 dims
+ *     divided by the row's scale (2^-100 where it is smaller) and rounded to
+ *     bf16; logits and probabilities take the scale.
  *   out [n_tok, H, D] F32 or BF16: bf16 tensor-core products (probabilities
  *     rounded to bf16), fp32 accumulation and softmax statistics.
  * Rows that a token does not see never reach its output, whatever they hold.

@@ -479,8 +479,10 @@ def _vector(what, name, g, n):
         raise CsaError(f"{what}: {name} must be a contiguous float32 [{n}]")
 
 
-def _like(t, dtype):
+def _like(what, t, dtype):
     """A new contiguous tensor of t's shape."""
+    if dtype is not None and dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise CsaError(f"{what}: out must be float32 or bfloat16")
     return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
@@ -543,7 +545,7 @@ def csa_rope(x, cu_q, q_pos, inv_freq, *, rope_start=None, interleaved=False, in
     r = _freqs(what, inv_freq)
     with _on(what, dev, stream):
         if out is None:
-            out = _like(x, out_dtype)
+            out = _like(what, x, out_dtype)
             ot, oh = H * D, D
         else:
             if out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
@@ -585,13 +587,13 @@ def csa_qk_norm_rope(q, k, cu_q, q_pos, inv_freq, *, q_gain=None, k_gain=None, r
     kot = Hk * D
     with _on(what, dev, stream):
         if q_out is None:
-            q_out = _like(q, out_dtype)
+            q_out = _like(what, q, out_dtype)
         else:
             _, _, _, qot, qoh = _out_heads(what, "q_out", q_out)
         if k is None:
             pass
         elif k_out is None:
-            k_out = _like(k, out_dtype)
+            k_out = _like(what, k, out_dtype)
         else:
             _, _, _, kot, koh = _out_heads(what, "k_out", k_out)
         if given:
@@ -707,9 +709,7 @@ def csa_paged_attention(q, cu_q, q_pos, *, tok_pages=None, tok_table=None, W=128
     _vector(what, "sink", sink, H)
     with _on(what, dev, stream):
         if out is None:
-            out = _like(q, out_dtype)
-            if out_dtype is not None and out_dtype not in (torch.float32, torch.bfloat16):
-                raise CsaError(f"{what}: out must be float32 or bfloat16")
+            out = _like(what, q, out_dtype)
         else:
             if out.shape != shape or out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or \
                     (out_dtype is not None and out.dtype != out_dtype):

@@ -216,10 +216,10 @@ struct SplitPlan {
 };
 __device__ __forceinline__ void make_plan(const AttnParams& p, SplitPlan& s, int tid, int nthreads) {
   for (int b = tid; b < p.n_seq; b += nthreads) {
-    const int len = p.cu_q[b + 1] - p.cu_q[b];
+    const int len = seq_len(p.cu_q, b, p.n_tok);
     // a token without rows still has one (empty) range, which tells the merge so
     s.nh[b] = len > 0 ? max(1, paged_half_chunks(p, p.q_pos[b], p.q_pos[b] + len - 1)) : 0;
-    s.first[b] = max(0, len);      // the lengths, until the prefix sums replace them
+    s.first[b] = len;              // the lengths, until the prefix sums replace them
   }
   __syncthreads();
   if (tid < 32) {
@@ -265,13 +265,12 @@ __device__ __forceinline__ bool locate_warp(const AttnParams& p, const SplitPlan
     if (plan) {
       it.b = find_seq_warp(plan->first, p.n_seq, item, lane);
       if (it.b < 0) return false;
-      const int c0 = p.cu_q[it.b], len = p.cu_q[it.b + 1] - c0;
-      const int f0 = plan->first[it.b], ns = (plan->first[it.b + 1] - f0) / len;
+      const int f0 = plan->first[it.b], ns = (plan->first[it.b + 1] - f0) / seq_len(p.cu_q, it.b, p.n_tok);
       it.t = (int)(item - f0) / ns;
       it.sp = (int)(item - f0) % ns;
-      it.bt = c0 + it.t;
+      it.bt = p.cu_q[it.b] + it.t;
       it.per = plan->per;
-      return it.bt >= 0 && it.bt < p.n_tok && p.q_pos[it.b] + it.t >= 0;
+      return p.q_pos[it.b] + it.t >= 0;
     }
     it.bt = item;
     it.b = find_seq_warp(p.cu_q, p.n_seq, item, lane);
@@ -1471,7 +1470,7 @@ paged_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, c
   if (b < 0 || h >= H) return;
   const int c0 = cu_q[b], f0 = plan[b];
   if (q_pos[b] + (bt - c0) < 0) return;
-  const int ns = (plan[b + 1] - f0) / (cu_q[b + 1] - c0);
+  const int ns = (plan[b + 1] - f0) / seq_len(cu_q, b, gridDim.x);
   const int64_t i0 = f0 + (bt - c0) * ns;
   if (i0 + ns > max_items) return;
   const float sk = sink ? sink[h] : -CUDART_INF_F;

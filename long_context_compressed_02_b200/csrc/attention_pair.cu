@@ -145,9 +145,9 @@ __device__ __forceinline__ void tma_load_pair_4d(void* dst, const CUtensorMap* m
 }
 // MMAs and their commits are issued by whole warps in convergent code, with the
 // instruction itself predicated on one elected lane: descriptors then stay in
-// uniform registers, and 8 MMAs with a wait and a commit issue at
-// the tensor pipe's rate (65 cycles an MMA; from a branch that one lane takes,
-// 84 in a bare loop and 97 to 130 in this kernel).
+// uniform registers, and 8 MMAs with a wait and a commit issue at the tensor
+// pipe's rate (65 cycles an MMA; from a branch that one lane takes, 84 in a bare
+// loop).
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
                "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
@@ -251,7 +251,7 @@ __device__ __forceinline__ void find_work(const PairParams& p, int64_t x, int la
   for (int b0 = p.n_seq - 1; b0 >= 0; b0 -= 32) {
     const int b = b0 - lane;
     int len = 0;
-    if (b >= 0) len = max(0, p.cu_q[b + 1] - p.cu_q[b]);
+    if (b >= 0) len = seq_len(p.cu_q, b, p.n_tok);
     const int tiles = (len + per - 1) / per;
     int inc = tiles;
 #pragma unroll
@@ -273,7 +273,6 @@ __device__ __forceinline__ void find_work(const PairParams& p, int64_t x, int la
     w.tok0 = (int64_t)p.cu_q[w.seq] + (int64_t)t * per;
     w.ntok = min(per, len - t * per);
     w.pos0 = p.q_pos[w.seq] + (int64_t)t * per;
-    if (w.tok0 < 0 || w.tok0 + w.ntok > p.n_tok) return;
     w.has = 1;
     const int64_t last = w.pos0 + w.ntok - 1;
 #pragma unroll

@@ -25,6 +25,12 @@ __device__ __forceinline__ int find_seq_warp(const int32_t* cu_q, int n_seq, int
   return lo;
 }
 
+// Tokens of sequence b that are rows of the batch, whatever cu_q holds.
+__device__ __forceinline__ int seq_len(const int32_t* cu_q, int b, int64_t n_tok) {
+  const int c0 = cu_q[b];
+  return c0 < 0 ? 0 : (int)max((int64_t)0, min((int64_t)cu_q[b + 1], n_tok) - c0);
+}
+
 // One paged cache: block_table [n_seq, max_pages] of page numbers, pages of
 // 2^ps_log2 rows.
 struct PageTable {

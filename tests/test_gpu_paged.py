@@ -408,6 +408,22 @@ def test_tokens_at_negative_positions_are_left_alone(csa):
         assert bool(((out[2:].float() - ref.float()).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("n,H,D,W", [(10, 64, 512, 0), (90, 64, 512, 0), (90, 8, 128, 128)])
+def test_batch_that_ends_inside_a_sequence(csa, n, H, D, W):
+    """cu_q names more rows than the tensors have: those below n_tok are worked on, none behind them."""
+    c = Case(lens=[n // 2, n], pos=[100, 40], H=H, D=D, W=W)
+    m = n
+    room = torch.full((c.n, H, D), 9.0, dtype=BF, device="cuda")
+    csa.csa_paged_attention(c.q[:m], c.cu, c.qp, out=room[:m], **c.kw)
+    w, _ = csa.csa_rope_freqs(64)
+    turned = torch.full_like(room, 9.0)
+    csa.csa_rope(c.q[:m], c.cu, c.qp, w, out=turned[:m])
+    csa.check_device_error()
+    c.check(room, only=[0, n // 2 - 1, n // 2, m - 1])
+    assert torch.equal(turned[:m], csa.csa_rope(c.q, c.cu, c.qp, w)[:m])
+    assert bool((room[m:] == 9.0).all()) and bool((turned[m:] == 9.0).all())
+
+
 def test_rows_out_of_sight_do_not_matter(csa):
     """A later token's NaN row reaches that token and those after it only, in decode-sized and chunk-sized batches."""
     for lens, H, D in (([12], 64, 512), ([110], 64, 512), ([110], 8, 128)):
@@ -542,6 +558,7 @@ def test_binding_refusals(csa):
     bad = [
         (lambda: csa.csa_rope(x, c.cu.long(), c.qp, w), "int32"), (lambda: csa.csa_rope(x, c.cu, c.qp[:0], w), "cu_q"),
         (lambda: csa.csa_rope(x, c.cu, c.qp, w.float()), "inv_freq"), (lambda: csa.csa_rope(x.half(), c.cu, c.qp, w), "float32 or bfloat16"),
+        (lambda: csa.csa_rope(x, c.cu, c.qp, w, out_dtype=torch.float16), "float32 or bfloat16"),
         (lambda: csa.csa_rope(x.transpose(1, 2), c.cu, c.qp, w), "last dimension"), (lambda: csa.csa_rope(x[..., :120], c.cu, c.qp, w), "multiple of 16"),
         (lambda: csa.csa_rope(x[:, 1:], c.cu, c.qp, w, out=x[:, :-1]), "overlap"), (lambda: csa.csa_rope(x, c.cu, c.qp, w, out=x[:1]), "shape"),
         (lambda: csa.csa_rope(x, c.cu, c.qp, w, out=x[:, :1].expand_as(x)), "overlap"),
