@@ -290,7 +290,26 @@ __device__ __forceinline__ bool locate_warp(const AttnParams& p, const SplitPlan
 // mbarrier.try_wait suspends the thread in hardware until the phase completes
 // (or a short system time limit passes), so the loop needs no sleep of its own;
 // the wall clock and the CTA's abort flag are checked every 64 polls.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t start = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_ns();
+      if (start == 0) start = now;
+      else if (now - start > kWaitNs) break;
+    }
+  }
+  *abort_flag = 1;
+  atomicOr(&g_err_attn, DEV_ERR_TIMEOUT_MBAR);
+  return false;
+}
+// SHORT: only the first try inlined, for the paged form, whose roles' code misses
+// the instruction caches.
+template <bool SHORT = false>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if constexpr (SHORT) return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag);
   uint64_t start = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -365,11 +384,6 @@ __device__ __forceinline__ void codes_to_bf16(uint4 raw, uint4& lo, uint4& hi, u
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
-}
-__device__ __forceinline__ bool has_nan_code(uint4 r) {
-  const uint32_t n = ((r.x & 0x7f7f7f7fu) + 0x01010101u) | ((r.y & 0x7f7f7f7fu) + 0x01010101u) |
-                     ((r.z & 0x7f7f7f7fu) + 0x01010101u) | ((r.w & 0x7f7f7f7fu) + 0x01010101u);
-  return (n & 0x80808080u) != 0;
 }
 // 8 bf16 times f
 __device__ __forceinline__ void bf16x8_scaled(uint4 raw, float f, float* v) {
@@ -469,6 +483,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
   int64_t* s_items = reinterpret_cast<int64_t*>(item_empty + 4);   // [4]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_items + 4);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
+  constexpr int kRoll = PAGED ? 1 : D / 128;         // unrolling of the loads' loops, see wait_bar
   constexpr bool kCodes = PAGED && KV == KV_FP8;     // slots hold e4m3 codes, row scales apart
   __shared__ float s_scale[kCodes ? 2 : 1][kRows];
 
@@ -511,12 +526,12 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     if (p.item_counter == nullptr) return (int64_t)blockIdx.x + (int64_t)k * gridDim.x;
     const uint32_t slot = k & 3, par = (k >> 2) & 1;
     if (fetcher) {
-      if (wait_bar(&item_empty[slot], par ^ 1, abort_flag)) s_items[slot] = (int64_t)atomicAdd(p.item_counter, 1u);
+      if (wait_bar<PAGED>(&item_empty[slot], par ^ 1, abort_flag)) s_items[slot] = (int64_t)atomicAdd(p.item_counter, 1u);
       else s_items[slot] = n_items;
       mbar_arrive(&item_full[slot]);
     }
     int64_t it = n_items;
-    if (wait_bar(&item_full[slot], par, abort_flag)) it = s_items[slot];
+    if (wait_bar<PAGED>(&item_full[slot], par, abort_flag)) it = s_items[slot];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&item_empty[slot]);
     return it;
@@ -540,7 +555,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per);
       if (rs.c1 <= rs.c0) continue;
       // ---- Q tile: 64 rows x NS slabs of 128 B
-      if (grp == 0 && !wait_bar(q_free, (qcount & 1) ^ 1, abort_flag)) { ok = false; break; }
+      if (grp == 0 && !wait_bar<PAGED>(q_free, (qcount & 1) ^ 1, abort_flag)) { ok = false; break; }
       ++qcount;
       if (grp != 0) {
         // the first group's
@@ -549,11 +564,13 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         // are zero-filled, and their columns are never written out)
         if (lt == 0) {
           mbar_expect_tx(q_full, kNQ * D * 2);
-          if constexpr (PAGED) tma_load_3d(sQ, &map_q, 0, (int32_t)(bt * p.H), 0, q_full);   // all slabs in one copy
-          else
+          if constexpr (PAGED) {
+            tma_load_3d(sQ, &map_q, 0, (int32_t)(bt * p.H), 0, q_full);      // all slabs in one copy
+          } else {
 #pragma unroll 1
-          for (int s = 0; s < NS; ++s)
-            tma_load_2d(sQ + s * kQSlab, &map_q, 64 * s, (int32_t)(bt * p.H), q_full);
+            for (int s = 0; s < NS; ++s)
+              tma_load_2d(sQ + s * kQSlab, &map_q, 64 * s, (int32_t)(bt * p.H), q_full);
+          }
         } else {
           mbar_arrive(q_full);
         }
@@ -590,51 +607,82 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       // ---- KV half chunks into the two-slot ring
       int pre_c = -1;                    // half chunk whose gathered row index pre_row holds
       int32_t pre_row = 0;
-      // Paged rows: bulk prefetch of a half chunk into L2, page by page.  The ring
-      // holds two half chunks, too few to cover the latency of HBM; kAhead + 1 half
-      // chunks ahead the loads find their rows in L2.
-      constexpr int kAhead = kCodes ? 4 : 1;
-      auto prefetch = [&](int cc) {
-        if (cc >= rs.c1) return;
+      // Paged rows.  Table entries are loaded one turn ahead of their use and kept as
+      // they are until then: every look-up that the copies wait for costs a turn
+      // 1,000 cycles and more (three of them took half of an e4m3 turn).
+      // Rows [r0, r1) of half chunk cc in its cache; cc < rs.c1.
+      struct Span { bool win; int r0, r1; };
+      auto span_of = [&](int cc) -> Span {
         const bool w = cc < rs.nh2;
-        const PageTable& pt = w ? p.pt2 : p.pt1;
-        const int64_t at = (int64_t)(w ? cc : cc - rs.nh2) * kRows;
-        const int64_t r0 = (w ? rs.lo2 : 0) + at, r1 = r0 + min((int64_t)kRows, (w ? rs.n2 : rs.n1) - at);
-        const int64_t pg1 = (r1 - 1) >> pt.ps_log2;
-        for (int64_t pg = (r0 >> pt.ps_log2) + lane; pg <= pg1; pg += 32) {
-          const int64_t a = max(r0, pg << pt.ps_log2), e = min(r1, (pg + 1) << pt.ps_log2);
-          const int64_t g0 = page_row(pt, b, a);
-          if (g0 < 0) continue;
-          const uint32_t n = (uint32_t)(e - a);
-          if (KV == KV_FP8 && !w) {
-            prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(p.kv) + g0 * (D - 64), n * (D - 64));
-            prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(p.kv_rope) + g0 * 128, n * 128);
-            if (pt.ps_log2 >= 2)         // whole 16-byte pieces lie within the page
-              prefetch_l2_bulk(p.kv_scale + (g0 & ~(int64_t)3), 4 * (uint32_t)(((g0 & 3) + n + 3) & ~3u));
-          } else {
-            prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(w ? p.kv2 : p.kv) + g0 * D * 2, n * (D * 2));
-          }
+        const int at = (w ? cc : cc - rs.nh2) * kRows, first = w ? (int)rs.lo2 : 0;
+        return Span{w, first + at, first + min(at + kRows, w ? rs.n2 : rs.n1)};
+      };
+      auto entry_at = [&](const Span& s, int page) {
+        const PageTable& pt = s.win ? p.pt2 : p.pt1;
+        return __ldg(pt.table + (int64_t)b * pt.max_pages + page);
+      };
+      // the entry of this lane's row 16 lw + lane % 16 of a half chunk (where a block
+      // lies within a page: of all its rows)
+      auto row_entry = [&](int cc) -> int32_t {
+        if (cc >= rs.c1) return -1;
+        const Span s = span_of(cc);
+        const int r = s.r0 + 16 * lw + (lane & 15);
+        return r < s.r1 ? entry_at(s, r >> (s.win ? p.pt2 : p.pt1).ps_log2) : -1;
+      };
+      // Bulk prefetch of a half chunk into L2, a page per lane (of the first 32).  The
+      // ring holds two half chunks, too few to cover the latency of HBM; kAhead + 1
+      // half chunks ahead the loads find their rows in L2.
+      constexpr int kAhead = kCodes ? 4 : 1;
+      auto page_entry = [&](int cc) -> int32_t {
+        if (cc >= rs.c1) return -1;
+        const Span s = span_of(cc);
+        const int ps = (s.win ? p.pt2 : p.pt1).ps_log2, pg = (s.r0 >> ps) + lane;
+        return pg <= (s.r1 - 1) >> ps ? entry_at(s, pg) : -1;
+      };
+      auto prefetch = [&](int cc, int32_t pg) {
+        const Span s = span_of(cc);
+        const PageTable& pt = s.win ? p.pt2 : p.pt1;
+        if (pg < 0 || pg >= pt.n_pages) return;
+        const int first = ((s.r0 >> pt.ps_log2) + lane) << pt.ps_log2;
+        const int a = max(s.r0, first), e = min((int64_t)s.r1, (int64_t)first + (1 << pt.ps_log2));
+        const int64_t g0 = ((int64_t)pg << pt.ps_log2) + (a - first);
+        const uint32_t n = (uint32_t)(e - a);
+        if (KV == KV_FP8 && !s.win) {
+          prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(p.kv) + g0 * (D - 64), n * (D - 64));
+          prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(p.kv_rope) + g0 * 128, n * 128);
+          if (pt.ps_log2 >= 2)         // whole 16-byte pieces lie within the page
+            prefetch_l2_bulk(p.kv_scale + (g0 & ~(int64_t)3), 4 * (uint32_t)(((g0 & 3) + n + 3) & ~3u));
+        } else {
+          prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(s.win ? p.kv2 : p.kv) + g0 * D * 2, n * (D * 2));
         }
       };
-      if (kCodes && grp == 0 && lw == 0)
-        for (int i = 1; i <= kAhead; ++i) prefetch(rs.c0 + i);
-      // The row of the page store where a half chunk starts, looked up one ahead
-      // of its use (a load's latency that the copies would wait for).
-      auto start_of = [&](int cc) -> int64_t {
-        if (cc >= rs.c1) return -1;
-        const bool w = cc < rs.nh2;
-        return page_row(w ? p.pt2 : p.pt1, b, (w ? rs.lo2 : 0) + (int64_t)(w ? cc : cc - rs.nh2) * kRows);
-      };
-      int64_t start = PAGED ? start_of(rs.c0 + (kCodes && (int)(g & 1) != grp ? 1 : 0)) : 0;
+      const int step = kCodes ? 2 : 1;              // half chunks between this group's turns
+      const int c_first = rs.c0 + (kCodes && (int)(g & 1) != grp ? 1 : 0);
+      // bf16: the second warp prefetches, so that the first's copies go out at once
+      const bool fetches = PAGED && lw == (kCodes ? 0 : 1);
+      int32_t row_next = -1, page_next = -1;
+      if constexpr (PAGED) {
+        row_next = row_entry(c_first);
+        if (fetches) {
+          int32_t pg[kAhead];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) pg[i] = kCodes && grp ? -1 : page_entry(rs.c0 + 1 + i);
+          page_next = page_entry(c_first + kAhead + 1);
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) prefetch(rs.c0 + 1 + i, pg[i]);
+        }
+      }
       for (int c = rs.c0; c < rs.c1 && ok; ++c, ++g) {
         if (kCodes && (int)(g & 1) != grp) continue;
-        const int64_t g0 = start;
-        if (PAGED) start = start_of(c + (kCodes ? 2 : 1));
-        // bf16: the second warp prefetches, so that the first's copies go out at once
-        if (PAGED && lw == (kCodes ? 0 : 1)) {
-          if (c == rs.c0 && !kCodes)
-            for (int i = 1; i <= kAhead; ++i) prefetch(rs.c0 + i);
-          prefetch(c + kAhead + 1);
+        int32_t row_pg = -1;
+        if constexpr (PAGED) {
+          row_pg = row_next;
+          row_next = row_entry(c + step);
+          if (fetches) {
+            const int32_t pg = page_next;
+            page_next = page_entry(c + step + kAhead + 1);
+            prefetch(c + kAhead + 1, pg);
+          }
         }
         const int slot = g & 1;
         const uint32_t fpar = ((g >> 1) & 1) ^ 1;     // completion of PV(g - 2), which read this slot
@@ -655,10 +703,11 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         bool tma;
         int32_t y0 = 0;
         if constexpr (PAGED) {
-          const int64_t r0 = (win ? rs.lo2 : 0) + (int64_t)cl * kRows;
-          tma = fullh && (r0 & (kRows - 1)) == 0 && (win ? p.tma_tok != 0 : p.tma_kv != 0);
-          tma = tma && g0 >= 0;
-          y0 = (int32_t)g0;
+          const PageTable& pt = win ? p.pt2 : p.pt1;
+          const int r0 = (win ? (int)rs.lo2 : 0) + cl * kRows;
+          tma = fullh && (r0 & (kRows - 1)) == 0 && (win ? p.tma_tok != 0 : p.tma_kv != 0) && row_pg >= 0 &&
+                row_pg < pt.n_pages;
+          y0 = (int32_t)((uint32_t)row_pg << pt.ps_log2) + (r0 & ((1 << pt.ps_log2) - 1));
         } else {
           tma = win ? (p.tma_tok != 0 && (p.src2 == SRC2_WINDOW || fullh))
                     : (rs.idx == nullptr && p.tma_kv != 0 && fullh);
@@ -666,15 +715,16 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
                    : (int32_t)((int64_t)b * p.cap + (int64_t)cl * kRows);
         }
         if (tma) {
+#pragma unroll kRoll
           for (int tt = 0; tt < NT; ++tt) {
-            if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
+            if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
             if (lt == 0) {
               mbar_expect_tx(&full[tt], 2 * kSlab);
               if constexpr (PAGED) {
                 tma_load_3d(sl_base + (2 * tt) * kSlab, win ? &map_tok : &map_kv, 0, y0, 2 * tt, &full[tt]);
               } else {
-              tma_load_2d(sl_base + (2 * tt) * kSlab, win ? &map_tok : &map_kv, 128 * tt, y0, &full[tt]);
-              tma_load_2d(sl_base + (2 * tt + 1) * kSlab, win ? &map_tok : &map_kv, 128 * tt + 64, y0, &full[tt]);
+                tma_load_2d(sl_base + (2 * tt) * kSlab, win ? &map_tok : &map_kv, 128 * tt, y0, &full[tt]);
+                tma_load_2d(sl_base + (2 * tt + 1) * kSlab, win ? &map_tok : &map_kv, 128 * tt + 64, y0, &full[tt]);
               }
             } else {
               mbar_arrive(&full[tt]);
@@ -701,8 +751,9 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           }
           if constexpr (PAGED) {
             // a row without a page is recorded and read as zeros
-            if (valid) row = page_row(win ? p.pt2 : p.pt1, b, row);
-            if (row < 0) { atomicOr(&g_err_attn, DEV_ERR_BAD_INDEX); valid = false; row = 0; }
+            const PageTable& pt = win ? p.pt2 : p.pt1;
+            if (valid && (row_pg < 0 || row_pg >= pt.n_pages)) { atomicOr(&g_err_attn, DEV_ERR_BAD_INDEX); valid = false; }
+            row = valid ? ((int64_t)row_pg << pt.ps_log2) + (row & ((1 << pt.ps_log2) - 1)) : 0;
           } else {
             row += win ? (int64_t)b * p.cap2 : (int64_t)b * p.cap;
           }
@@ -710,8 +761,9 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           // Slab pair tt is signalled once this thread's copies of it have landed
           // (cp.async group tt), fenced to the async proxy here, on the producer
           // side, so the MMA issuer needs no proxy fence of its own.
+#pragma unroll kRoll
           for (int tt = 0; tt < NT; ++tt) {
-            if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
+            if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
             gather16_bf16(rp, valid, 2 * tt, sl_base + (2 * tt) * kSlab, 16 * lw, lane);
             gather16_bf16(rp, valid, 2 * tt + 1, sl_base + (2 * tt + 1) * kSlab, 16 * lw, lane);
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -727,7 +779,106 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           mbar_arrive(&full[NT - 1]);
           continue;
         }
-        if (KV == KV_FP8 && !win) {
+        if constexpr (kCodes) {
+          // e4m3 pages: the lanes and pieces of the form below.  The slot takes the
+          // codes themselves (exact in bf16) and the RoPE part divided by the row's
+          // scale; the softmax multiplies logits and probabilities by the scale, so
+          // the nope dims are rounded nowhere and a code costs 5 integer instructions
+          // for 2 instead of conversions through float32.  Scales below 2^-100 count
+          // as 2^-100: their rows' codes are worth nothing next to any RoPE part,
+          // which must not overflow.  The pairs of slabs but the last take one rolled
+          // loop, which loads one pair ahead: the code of all of them with their loads
+          // in flight at once missed the instruction caches (32 sequences of 512 to 8,192
+          // entries: 76 us, 70 so).
+          constexpr int kNope = D - 64;
+          const int rl = lane & 15;
+          const PageTable& pt = p.pt1;
+          const int r1 = cl * kRows + 16 * lw + rl;
+          int64_t row = -1;                      // row 16 lw + rl of the half chunk: row of the store
+          if (r1 < rs.n1) {
+            if (row_pg >= 0 && row_pg < pt.n_pages) row = ((int64_t)row_pg << pt.ps_log2) + (r1 & ((1 << pt.ps_log2) - 1));
+            else atomicOr(&g_err_attn, DEV_ERR_BAD_INDEX);
+          }
+          float sc = row >= 0 ? __ldg(p.kv_scale + row) : 0.f;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          const uint8_t* at[4];                  // piece l & 7 of rows 4 i + l / 8; null: zeros
+          uint4 raw[4], next[4], tail[2], rope[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int64_t gr = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
+            at[i] = gr >= 0 ? reinterpret_cast<const uint8_t*>(p.kv) + gr * kNope + 16 * (lane & 7) : nullptr;
+            if (NT > 1) raw[i] = at[i] ? __ldg(reinterpret_cast<const uint4*>(at[i])) : zero;
+            rope[i] = at[i] ? __ldg(reinterpret_cast<const uint4*>(p.kv_rope + gr * 64 + 8 * (lane & 7))) : zero;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int64_t gr = __shfl_sync(0xffffffffu, row, 8 * i + (lane >> 2));
+            tail[i] = gr >= 0 ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p.kv) + gr * kNope +
+                                                                     128 * (NT - 1) + 16 * (lane & 3)))
+                              : zero;
+          }
+          uint32_t nan[4] = {0, 0, 0, 0}, nan_tail[2] = {0, 0};
+          // lanes of a pair's second slab store their odd piece first: the two slabs lie
+          // on the same banks
+          const int odd = (lane >> 2) & 1;
+#pragma unroll 1
+          for (int tt = 0; tt < NT - 1; ++tt) {
+            if (tt + 1 < NT - 1)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                next[i] = at[i] ? __ldg(reinterpret_cast<const uint4*>(at[i] + 128 * (tt + 1))) : zero;
+            if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
+            uint8_t* dst = sl_base + (2 * tt + odd) * kSlab;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rr = 16 * lw + 4 * i + (lane >> 3);
+              const uint4 w = raw[i];
+              uint4 one, two;
+              codes_to_bf16(odd ? make_uint4(w.z, w.w, w.x, w.y) : w, one, two, nan[i]);
+              st_shared16(dst + swz128(rr, 2 * (lane & 3) + odd), one);
+              st_shared16(dst + swz128(rr, 2 * (lane & 3) + 1 - odd), two);
+              raw[i] = next[i];
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&full[tt]);
+          }
+          if (!ok || !wait_bar<PAGED>(&done[NT - 1], fpar, abort_flag)) { ok = false; break; }
+          uint8_t* dst = sl_base + (NS - 2) * kSlab;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = 16 * lw + 8 * i + (lane >> 2);
+            uint4 lo, hi;
+            codes_to_bf16(tail[i], lo, hi, nan_tail[i]);
+            st_shared16(dst + swz128(rr, 2 * (lane & 3)), lo);
+            st_shared16(dst + swz128(rr, 2 * (lane & 3) + 1), hi);
+          }
+          sc = fabsf(sc) < 0x1p-100f ? 0x1p-100f : sc;
+          const float isc = 1.f / sc;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = __shfl_sync(0xffffffffu, isc, 4 * i + (lane >> 3));
+            float v[8];
+            bf16x8_scaled(rope[i], f, v);
+            st_shared16(dst + kSlab + swz128(16 * lw + 4 * i + (lane >> 3), lane & 7), to_bf16x8(v));
+          }
+          // A NaN code has become a number: its row's scale carries it instead.
+          if (__any_sync(0xffffffffu, ((nan[0] | nan[1] | nan[2] | nan[3] | nan_tail[0] | nan_tail[1]) & 0x80808080u) != 0)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const unsigned m = __ballot_sync(0xffffffffu, (nan[i] & 0x80808080u) != 0);      // rows 4 i + l / 8
+              if (rl / 4 == i && ((m >> ((rl % 4) * 8)) & 0xffu)) sc = CUDART_NAN_F;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const unsigned m = __ballot_sync(0xffffffffu, (nan_tail[i] & 0x80808080u) != 0); // rows 8 i + l / 4
+              if (rl / 8 == i && ((m >> ((rl % 8) * 4)) & 0xfu)) sc = CUDART_NAN_F;
+            }
+          }
+          if (lane < 16) s_scale[slot][16 * lw + rl] = sc;
+          fence_proxy_async_smem();
+          mbar_arrive(&full[NT - 1]);
+          continue;
+        } else if (KV == KV_FP8 && !win) {
           // e4m3 rows: nope part (D - 64 bytes), bf16 RoPE part (64 dims), fp32
           // row scale.  Loader warp lw owns rows 16 lw .. 16 lw + 15 of the half
           // chunk; lane l looks up row 16 lw + (l & 15).  The loads are
@@ -747,12 +898,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
             const int r1 = (cc - rs.nh2) * kRows + 16 * lw + rl;
             bool vld = r1 < rs.n1;
             int64_t row1 = 0;
-            if constexpr (PAGED) {
-              if (vld) {
-                row1 = page_row(p.pt1, b, r1);
-                if (row1 < 0) { atomicOr(&g_err_attn, DEV_ERR_BAD_INDEX); vld = false; row1 = 0; }
-              }
-            } else if (vld) {
+            if (vld) {
               if (rs.idx) {
                 row1 = pre_c == cc ? pre_row : __ldg(rs.idx + r1);
                 if (row1 < 0 || row1 >= p.cap) { atomicOr(&g_err_attn, DEV_ERR_BAD_INDEX); vld = false; row1 = 0; }
@@ -760,7 +906,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
                 row1 = r1;
               }
             }
-            const long long gr0 = PAGED ? row1 : (long long)b * p.cap + row1;
+            const long long gr0 = (long long)b * p.cap + row1;
             scv = vld ? __ldg(p.kv_scale + gr0) : 0.f;
             const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -793,9 +939,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           if (c + 1 < rs.c1) {
             const int r0 = (c + 1 - rs.nh2) * kRows;
             const int nr = min(kRows, rs.n1 - r0);
-            if constexpr (PAGED) {
-              // prefetched above
-            } else if (rs.idx == nullptr) {
+            if (rs.idx == nullptr) {
               const long long g0 = (long long)b * p.cap + r0;
               if (lt == 0) prefetch_l2_bulk(kvn + g0 * kNope, (uint32_t)(nr * kNope));
               else if (lt == 1) prefetch_l2_bulk(kvr + g0 * 128, (uint32_t)(nr * 128));
@@ -805,67 +949,6 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
               pre_c = c + 1;
             }
           }
-          if constexpr (kCodes) {
-            // The slot takes the codes themselves (exact in bf16) and the RoPE part
-            // divided by the row's scale; the softmax multiplies logits and
-            // probabilities by the scale, so the nope dims are rounded nowhere and a
-            // code costs 5 integer instructions for 2 instead of conversions through
-            // float32.  Scales below 2^-100 count as 2^-100: their rows' codes are
-            // worth nothing next to any RoPE part, which must not overflow.
-            sc = fabsf(sc) < 0x1p-100f ? 0x1p-100f : sc;
-            const float isc = 1.f / sc;
-            uint32_t nan = 0;
-#pragma unroll
-            for (int tt = 0; tt < NT; ++tt) {
-              if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
-              if (tt < NT - 1) {
-                uint8_t* dst = sl_base + (2 * tt + ((lane & 7) >> 2)) * kSlab;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int rr = 16 * lw + 4 * i + (lane >> 3);
-                  uint4 lo, hi;
-                  codes_to_bf16(raw[tt][i], lo, hi, nan);
-                  st_shared16(dst + swz128(rr, 2 * (lane & 3)), lo);
-                  st_shared16(dst + swz128(rr, 2 * (lane & 3) + 1), hi);
-                }
-              } else {
-                uint8_t* dst = sl_base + (2 * tt) * kSlab;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const int rr = 16 * lw + 8 * i + (lane >> 2);
-                  uint4 lo, hi;
-                  codes_to_bf16(raw[tt][i], lo, hi, nan);
-                  st_shared16(dst + swz128(rr, 2 * (lane & 3)), lo);
-                  st_shared16(dst + swz128(rr, 2 * (lane & 3) + 1), hi);
-                }
-                uint8_t* dr = sl_base + (NS - 1) * kSlab;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float f = __shfl_sync(0xffffffffu, isc, 4 * i + (lane >> 3));
-                  float v[8];
-                  bf16x8_scaled(rope[i], f, v);
-                  st_shared16(dr + swz128(16 * lw + 4 * i + (lane >> 3), lane & 7), to_bf16x8(v));
-                }
-                // A NaN code has become a number: its row's scale carries it instead.
-                // Lane l's pieces belong to rows 4 i + l / 8 (all pairs but the last)
-                // and 8 i + l / 4, so a warp with a NaN looks each piece up again.
-                if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0)) {
-#pragma unroll
-                  for (int t2 = 0; t2 < NT; ++t2)
-#pragma unroll
-                    for (int i = 0; i < (t2 < NT - 1 ? 4 : 2); ++i) {
-                      const unsigned m = __ballot_sync(0xffffffffu, has_nan_code(raw[t2][i]));
-                      const int per = t2 < NT - 1 ? 8 : 4, rows = 32 / per;
-                      if (rl / rows == i && ((m >> ((rl % rows) * per)) & ((1u << per) - 1u))) sc = CUDART_NAN_F;
-                    }
-                }
-                if (lane < 16) s_scale[slot][16 * lw + rl] = sc;
-              }
-              fence_proxy_async_smem();
-              mbar_arrive(&full[tt]);
-            }
-            continue;
-          }
           // row scales to the converting lanes (waits for the scale loads only now)
           float sc4[4], sc2[2];
 #pragma unroll
@@ -874,7 +957,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           for (int i = 0; i < 2; ++i) sc2[i] = __shfl_sync(0xffffffffu, sc, 8 * i + (lane >> 2));
 #pragma unroll
           for (int tt = 0; tt < NT; ++tt) {
-            if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
+            if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
             if (tt < NT - 1) {
               // piece l & 7 of the pair: slab 2 tt + (l & 7) / 4, 16-byte chunks 2 (l & 3), 2 (l & 3) + 1
               uint8_t* dst = sl_base + (2 * tt + ((lane & 7) >> 2)) * kSlab;
@@ -930,7 +1013,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
             const float4 a = valid ? __ldg(reinterpret_cast<const float4*>(src + 64 * s) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
             v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
           }
-          if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
+          if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
           store_row_slab_f32(sl_base + s * kSlab, my_r, v);
           fence_proxy_async_smem();
           mbar_arrive(&full[tt]);
@@ -949,7 +1032,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     // Paged calls issue from whole warps, the instruction alone predicated on one
     // elected lane: in convergent code the descriptors stay in uniform registers.
     auto wait_issuer = [&](uint64_t* bar, uint32_t parity) {
-      const bool r = wait_bar(bar, parity, abort_flag);
+      const bool r = wait_bar<PAGED>(bar, parity, abort_flag);
       return PAGED ? __all_sync(0xffffffffu, r) != 0 : r;
     };
     auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
@@ -1081,7 +1164,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       for (int i = 0; i < 16; ++i) l_part[i] = 0.f;
       for (int c = rs.c0; c < rs.c1 && ok; ++c, ++g) {
         const uint32_t sb = g & 1;
-        if (!wait_bar(&s_full[sb], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+        if (!wait_bar<PAGED>(&s_full[sb], (g >> 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         float x[32], xb[32];
         tmem_ld16x256b_x8(tmem + lane_base + 64 * sb, x);
@@ -1098,7 +1181,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         float scA = 1.f, scB = 1.f;
         if (kCodes && !win) {
           // the scales came with the slot's last slab pair (complete: S was made from it)
-          if (!wait_bar(&kv_full[sb * NT + NT - 1], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+          if (!wait_bar<PAGED>(&kv_full[sb * NT + NT - 1], (g >> 1) & 1, abort_flag)) { ok = false; break; }
           scA = s_scale[sb][rA];
           scB = s_scale[sb][rB];
 #pragma unroll
@@ -1177,7 +1260,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         }
         // P^T rows rA, rB -> this half chunk's buffer (MN-major B operand of PV),
         // free once PV(g - 2) has retired
-        if (!wait_bar(&pv_done[sb * NT + NT - 1], ((g >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+        if (!wait_bar<PAGED>(&pv_done[sb * NT + NT - 1], ((g >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
         const uint32_t pb = smem_u32(sP + sb * kPBuf) + 4 * (lane & 3);
 #pragma unroll
         for (int cc = 0; cc < 8; ++cc) {
@@ -1198,7 +1281,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           // O^T columns scale by alpha once PV(g - 1) has retired (this thread is
           // TMEM lane e of every tile)
           const uint32_t gp = g - 1;
-          if (!wait_bar(&pv_done[(gp & 1) * NT + NT - 1], (gp >> 1) & 1, abort_flag)) { ok = false; break; }
+          if (!wait_bar<PAGED>(&pv_done[(gp & 1) * NT + NT - 1], (gp >> 1) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
           for (int tt = 0; tt < NT; ++tt) {
 #pragma unroll
@@ -1254,7 +1337,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       const bool any = rs.c1 > rs.c0;
       if (any) {
         const uint32_t gl = g - 1;               // last half chunk of this item
-        if (!wait_bar(&pv_done[(gl & 1) * NT + NT - 1], (gl >> 1) & 1, abort_flag)) { ok = false; break; }
+        if (!wait_bar<PAGED>(&pv_done[(gl & 1) * NT + NT - 1], (gl >> 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
       }
       // Each thread is TMEM lane e of every O^T tile, i.e. output dim d = 128 tt + e

@@ -93,8 +93,10 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
                :: "r"(smem_u32(bar)) : "memory");
 }
 // Bounded wait on a barrier of this CTA's; gives up after kWaitNs or once
-// another warp of the CTA has.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+// another warp of the CTA has.  Only the first try is inlined, and the roles'
+// loops are not unrolled: seven roles' code shares the instruction caches, and a
+// third of the fetches from them missed (chunk over all raw rows 925 us, 870 so).
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   uint64_t start = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -108,6 +110,9 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   *abort_flag = 1;
   atomicOr(&g_err_pair, DEV_ERR_TIMEOUT_MBAR);
   return false;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag);
 }
 // The same, announcing `bytes` of copies that complete there.
 __device__ __forceinline__ void expect_leader(uint64_t* bar, uint32_t bytes) {
@@ -442,6 +447,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       const int n = max(0, min(2, blocks_of(x.w, x.i) - 2 * (int)cta));
       const bool mine = t.on && (kb >> 1) == (int)cta;
       const CUtensorMap* map = t.s ? &maps.k[1] : &maps.k[0];
+#pragma unroll 1
       for (int d = 0; d < kKStages; ++d, ++st) {
         const uint32_t sl = st % kStages;
         ok = wait_warp(&empty_k[sl], ((st / kStages) & 1) ^ 1, abort_flag);
@@ -464,6 +470,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       const CUtensorMap* map = t.s ? &maps.v[1] : &maps.v[0];
       const CUtensorMap* part = t.s ? &maps.k[1] : &maps.k[0];
       const int nv = 2 * blocks_of(x.w, x.i);
+#pragma unroll 1
       for (int v = 0; v < nv; ++v, ++st) {                   // dims 256 (v & 1) + 128 cta .. of block v / 2
         const uint32_t sl = st % kStages;
         ok = wait_warp(&empty_v[sl], ((st / kStages) & 1) ^ 1, abort_flag);
@@ -498,6 +505,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
     Stream x;
     while (ok && advance(x, 2, 64)) {
       const int nbk = blocks_of(x.w, x.i);
+#pragma unroll 1
       for (int v = 0; v < 2 * nbk; ++v, ++st) {
         const int kb = kTileBlocks * x.i + (v >> 1);
         if (block_clean(x.w, kb)) continue;
@@ -541,6 +549,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       ok = ok && (t < 2 || wait_warp(pv_sent, t & 1, abort_flag));       // behind PV(t - 2)
       ok = ok && wait_warp(&s_free[t & 1], ((t >> 1) & 1) ^ 1, abort_flag);
       if (!ok) continue;
+#pragma unroll 1
       for (int d = 0; d < kKStages; ++d, ++st) {
         const uint32_t sl = st % kStages;
         ok = wait_warp(&full_k[sl], (st / kStages) & 1, abort_flag);
@@ -571,6 +580,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
       ok = ok && wait_warp(p_full, t & 1, abort_flag);
       if (!ok) continue;
       const int nv = 2 * blocks_of(x.w, x.i);
+#pragma unroll 1
       for (int v = 0; v < nv; ++v, ++st) {
         const uint32_t sl = st % kStages;
         ok = wait_warp(&full_v[sl], (st / kStages) & 1, abort_flag);
