@@ -68,11 +68,12 @@ uint32_t read_clear_err_attention() {
 namespace {
 
 constexpr int kThreads = 352;      // 11 warps: 4 softmax + epilogue, 4 loaders, 3 MMA issuers
-// Paged e4m3 calls have a second group of 4 loader warps (11 - 14): the groups
-// take alternate half chunks, so one group's loads are in flight while the other
-// converts.
-template <int KV, bool PAGED>
-constexpr int attn_threads() { return PAGED && KV == 2 /* e4m3 */ ? kThreads + 128 : kThreads; }
+// Paged calls have 4 more warps (11 - 14).  E4M3: a second group of loaders; the
+// groups take alternate half chunks, so one group's loads are in flight while the
+// other converts.  BF16: a second group for the softmax and the output, with
+// columns (heads) 32 .. 63, which it does to 0 .. 31 of the first (@@).
+template <bool PAGED>
+constexpr int attn_threads() { return PAGED ? kThreads + 128 : kThreads; }
 constexpr int kNQ = 64;            // query rows (heads) per tile = MMA N
 constexpr int kRows = 64;          // KV rows per ring slot (a half chunk) = M of the S MMA
 constexpr float kTau = 8.0f;       // lazy-rescale threshold (log2 units)
@@ -440,9 +441,27 @@ __device__ __forceinline__ float2 col_reduce16(float (&v)[16], int lane) {
   }
   return make_float2(v[0], v[1]);
 }
+// The same for 32 columns, 8 values a thread: lane l gets column
+// 8 (l / 8) + 2 (l % 4) + (l / 4) % 2.
+template <bool MAX>
+__device__ __forceinline__ float col_reduce8(float (&v)[8], int lane) {
+#pragma unroll
+  for (int lv = 0; lv < 3; ++lv) {
+    const int off = 16 >> lv, n = 4 >> lv;
+    const bool up = (lane & off) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = up ? v[i + n] : v[i];
+      const float send = up ? v[i] : v[i + n];
+      const float got = __shfl_xor_sync(0xffffffffu, send, off);
+      v[i] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  return v[0];
+}
 
 template <int D, int KV, int EPI, bool PAGED = false>
-__global__ void __launch_bounds__(attn_threads<KV, PAGED>(), 1)
+__global__ void __launch_bounds__(attn_threads<PAGED>(), 1)
 attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_q,
             const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_tok) {
   constexpr int NS = D / 64;                 // 128-byte slabs per row
@@ -485,6 +504,8 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
   constexpr int kRoll = PAGED ? 1 : D / 128;         // unrolling of the loads' loops, see wait_bar
   constexpr bool kCodes = PAGED && KV == KV_FP8;     // slots hold e4m3 codes, row scales apart
+  constexpr bool kTwo = PAGED && !kCodes;            // two groups of softmax warps, 32 columns each
+  constexpr int kSoft = kTwo ? 256 : 128;            // their threads
   __shared__ float s_scale[kCodes ? 2 : 1][kRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -493,9 +514,9 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
   if (EPI == EPI_COMBINE && p.inv_rope && tid < 32)
     s_invf[tid] = exp(-2.0 * (double)tid / (double)p.rope_dim * log((double)p.rope_base));
   if (tid == 0) {
-    mbar_init(q_full, 128); mbar_init(q_free, 2); mbar_init(epi_done, 128);
+    mbar_init(q_full, 128); mbar_init(q_free, 2); mbar_init(epi_done, kSoft);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 2); mbar_init(&s_free[i], 128); mbar_init(&p_full[i], 128);
+      mbar_init(&s_full[i], 2); mbar_init(&s_free[i], kSoft); mbar_init(&p_full[i], kSoft);
       for (int t = 0; t < NT; ++t) { mbar_init(&kv_full[i * NT + t], 128); mbar_init(&pv_done[i * NT + t], 1); }
     }
     for (int i = 0; i < 4; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 11); }
@@ -537,7 +558,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     return it;
   };
 
-  if ((warp >= 4 && warp < 8) || warp >= 11) {
+  if ((warp >= 4 && warp < 8) || (kCodes && warp >= 11)) {
     // ============================ loaders
     const int grp = warp >= 11 ? 1 : 0;
     const int lt = grp ? tid - 352 : tid - 128;   // 0..127 of the group
@@ -1020,7 +1041,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         }
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 8 && warp < 11) {
     // ============================ MMA issuers (lane 0; each warp computes row sets)
     // S^T(h) = KV_h[64 rows, D] . Q^T        M 64, N 64, into TMEM columns 64 (h % 2)
     //          (+ 128 for the odd slabs' accumulator)
@@ -1131,12 +1152,25 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     // rows 16w .. 16w + 15.  tcgen05.ld 16x256b gives thread l rows
     // 16w + l/4 and 16w + l/4 + 8 of columns 8c + 2(l%4) + {0, 1}; column
     // statistics end up owned by lane l for columns 2l, 2l + 1.
-    const int e = tid;                        // TMEM lane of the O^T tiles = d-row
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    float* bc_m = s_bc + warp * 192;          // per-warp broadcast: [0,64) max, [64,128) alpha / coef_w, [128,192) coef_p
-    const int rA = 16 * warp + (lane >> 2), rB = rA + 8;
+    // With two groups a thread has 32 columns from col0 on, and a lane owns one.
+    constexpr int NC = kTwo ? 32 : 64, kOwn = NC / 32;
+    const int quad = warp & 3;                // a warp reads the TMEM lanes of its number modulo 4
+    const int grp = kTwo && warp >= 11 ? 1 : 0, col0 = 32 * grp, bar1 = 1 + 3 * grp, bar2 = 2 + 3 * grp;
+    const int e = 32 * quad + lane;           // TMEM lane of the O^T tiles = d-row
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    // per-warp broadcast: [0, NC) max, [NC, 2 NC) alpha / coef_w, [2 NC, 3 NC) coef_p
+    float* bc_m = s_bc + (4 * grp + quad) * 3 * NC;
+    const int own = kTwo ? 8 * (lane >> 3) + 2 * (lane & 3) + ((lane >> 2) & 1) : 2 * lane;   // first owned column
+    const int rA = 16 * quad + (lane >> 2), rB = rA + 8;
     uint32_t g = 0, icount = 0;
     bool ok = true;
+    // Maxima or sums of the columns over this warp's rows; red[w * NC + column] has
+    // warp w's then, for all of the group.
+    auto reduce_columns = [&](auto max, auto& v, float* red) {
+      if constexpr (kTwo) red[quad * NC + own] = col_reduce8<decltype(max)::value>(v, lane);
+      else *reinterpret_cast<float2*>(red + quad * NC + own) = col_reduce16<decltype(max)::value>(v, lane);
+      named_bar_sync(bar1, 128);
+    };
     for (uint32_t kk = 0; ok; ++kk) {
       const int64_t item = get_item(kk, false);
       if (item >= n_items) break;
@@ -1156,22 +1190,29 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         sincosf((float)r, &sf, &cf);
         cs[tid] = make_float2(cf, sf);
       }
-      float m_own[2] = {-CUDART_INF_F, -CUDART_INF_F};   // running max of columns 2 lane, 2 lane + 1
-      // this thread's rows' running sums of its 16 columns (v16 layout), reduced
-      // over the rows once, in the epilogue
-      float l_part[16];
+      float m_own[kOwn];                                 // running max of the owned columns
 #pragma unroll
-      for (int i = 0; i < 16; ++i) l_part[i] = 0.f;
+      for (int j = 0; j < kOwn; ++j) m_own[j] = -CUDART_INF_F;
+      // this thread's rows' running sums of its NC / 4 columns (layout of v), reduced
+      // over the rows once, in the epilogue
+      float l_part[NC / 4];
+#pragma unroll
+      for (int i = 0; i < NC / 4; ++i) l_part[i] = 0.f;
       for (int c = rs.c0; c < rs.c1 && ok; ++c, ++g) {
         const uint32_t sb = g & 1;
         if (!wait_bar<PAGED>(&s_full[sb], (g >> 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        float x[32], xb[32];
-        tmem_ld16x256b_x8(tmem + lane_base + 64 * sb, x);
-        tmem_ld16x256b_x8(tmem + lane_base + 128 + 64 * sb, xb);
+        float x[NC / 2], xb[NC / 2];
+        if constexpr (kTwo) {
+          tmem_ld16x256b_x4(tmem + lane_base + 64 * sb + col0, x);
+          tmem_ld16x256b_x4(tmem + lane_base + 128 + 64 * sb + col0, xb);
+        } else {
+          tmem_ld16x256b_x8(tmem + lane_base + 64 * sb, x);
+          tmem_ld16x256b_x8(tmem + lane_base + 128 + 64 * sb, xb);
+        }
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] += xb[i];
+        for (int i = 0; i < NC / 2; ++i) x[i] += xb[i];
         tc_fence_before();
         mbar_arrive(&s_free[sb]);
         const bool win = c < rs.nh2;
@@ -1185,13 +1226,13 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           scA = s_scale[sb][rA];
           scB = s_scale[sb][rB];
 #pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
+          for (int cc = 0; cc < NC / 8; ++cc) {
             x[4 * cc] *= scA; x[4 * cc + 1] *= scA;
             x[4 * cc + 2] *= scB; x[4 * cc + 3] *= scB;
           }
         }
 #pragma unroll
-        for (int cc = 0; cc < 8; ++cc) {                   // raw logits; scale folded below
+        for (int cc = 0; cc < NC / 8; ++cc) {                   // raw logits; scale folded below
           if (!vA) { x[4 * cc] = -CUDART_INF_F; x[4 * cc + 1] = -CUDART_INF_F; }
           if (!vB) { x[4 * cc + 2] = -CUDART_INF_F; x[4 * cc + 3] = -CUDART_INF_F; }
         }
@@ -1203,55 +1244,52 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         bool exceed = c == rs.c0;
         if (!exceed) {
 #pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
+          for (int cc = 0; cc < NC / 8; ++cc) {
             const float2 mm = *reinterpret_cast<const float2*>(bc_m + 8 * cc + 2 * (lane & 3));
             exceed |= fmaxf(x[4 * cc], x[4 * cc + 2]) * sl2 > mm.x + kTau;
             exceed |= fmaxf(x[4 * cc + 1], x[4 * cc + 3]) * sl2 > mm.y + kTau;
           }
         }
-        exceed = named_bar_or(2, 128, exceed);
+        exceed = named_bar_or(bar2, 128, exceed);
         bool need_rescale = false;
         if (exceed) {
-          float v16[16];
+          float v[NC / 4];
 #pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
-            v16[2 * cc] = fmaxf(x[4 * cc], x[4 * cc + 2]);
-            v16[2 * cc + 1] = fmaxf(x[4 * cc + 1], x[4 * cc + 3]);
+          for (int cc = 0; cc < NC / 8; ++cc) {
+            v[2 * cc] = fmaxf(x[4 * cc], x[4 * cc + 2]);
+            v[2 * cc + 1] = fmaxf(x[4 * cc + 1], x[4 * cc + 3]);
           }
-          const float2 cm = col_reduce16<true>(v16, lane);
-          float* red = s_red + (g & 1) * 256;
-          *reinterpret_cast<float2*>(red + warp * 64 + 2 * lane) = cm;
-          named_bar_sync(1, 128);
-          float alpha[2];
-          const float2 r0 = *reinterpret_cast<const float2*>(red + 2 * lane);
-          const float2 r1 = *reinterpret_cast<const float2*>(red + 64 + 2 * lane);
-          const float2 r2 = *reinterpret_cast<const float2*>(red + 128 + 2 * lane);
-          const float2 r3 = *reinterpret_cast<const float2*>(red + 192 + 2 * lane);
-          const float mx[2] = {fmaxf(fmaxf(r0.x, r1.x), fmaxf(r2.x, r3.x)) * sl2,
-                               fmaxf(fmaxf(r0.y, r1.y), fmaxf(r2.y, r3.y)) * sl2};
+          float* red = s_red + (g & 1) * 256 + grp * 128;
+          reduce_columns(std::true_type(), v, red);
+          float alpha[kOwn];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float mn = (mx[j] > m_own[j] + kTau) ? mx[j] : m_own[j];
+          for (int j = 0; j < kOwn; ++j) {
+            const float* r = red + own + j;
+            const float mx = fmaxf(fmaxf(r[0], r[NC]), fmaxf(r[2 * NC], r[3 * NC])) * sl2;
+            const float mn = (mx > m_own[j] + kTau) ? mx : m_own[j];
             alpha[j] = exp2f(m_own[j] - mn);             // 0 on the first half chunk
             if (mn != m_own[j] && c > rs.c0) need_rescale = true;
             m_own[j] = mn;
           }
           __syncwarp();
-          *reinterpret_cast<float2*>(bc_m + 2 * lane) = make_float2(m_own[0], m_own[1]);
-          *reinterpret_cast<float2*>(bc_m + 64 + 2 * lane) = make_float2(alpha[0], alpha[1]);
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            bc_m[own + j] = m_own[j];
+            bc_m[NC + own + j] = alpha[j];
+          }
           need_rescale = __any_sync(0xffffffffu, need_rescale);
           __syncwarp();
           // the running sums of this thread's columns scale by the same factors
 #pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
-            const float2 al = *reinterpret_cast<const float2*>(bc_m + 64 + 8 * cc + 2 * (lane & 3));
+          for (int cc = 0; cc < NC / 8; ++cc) {
+            const float2 al = *reinterpret_cast<const float2*>(bc_m + NC + 8 * cc + 2 * (lane & 3));
             l_part[2 * cc] *= al.x;
             l_part[2 * cc + 1] *= al.y;
           }
         }
-        float pr[32];
+        float pr[NC / 2];
 #pragma unroll
-        for (int cc = 0; cc < 8; ++cc) {
+        for (int cc = 0; cc < NC / 8; ++cc) {
           const float2 mm = *reinterpret_cast<const float2*>(bc_m + 8 * cc + 2 * (lane & 3));
           pr[4 * cc + 0] = fast_exp2(fmaf(x[4 * cc + 0], sl2, -mm.x));
           pr[4 * cc + 1] = fast_exp2(fmaf(x[4 * cc + 1], sl2, -mm.y));
@@ -1263,17 +1301,17 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         if (!wait_bar<PAGED>(&pv_done[sb * NT + NT - 1], ((g >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
         const uint32_t pb = smem_u32(sP + sb * kPBuf) + 4 * (lane & 3);
 #pragma unroll
-        for (int cc = 0; cc < 8; ++cc) {
+        for (int cc = 0; cc < NC / 8; ++cc) {
           if constexpr (kCodes) {       // the row's scale goes into its probabilities
-            st_shared4(pb + swz128(rA, cc), pack_bf16(pr[4 * cc] * scA, pr[4 * cc + 1] * scA));
-            st_shared4(pb + swz128(rB, cc), pack_bf16(pr[4 * cc + 2] * scB, pr[4 * cc + 3] * scB));
+            st_shared4(pb + swz128(rA, cc + 4 * grp), pack_bf16(pr[4 * cc] * scA, pr[4 * cc + 1] * scA));
+            st_shared4(pb + swz128(rB, cc + 4 * grp), pack_bf16(pr[4 * cc + 2] * scB, pr[4 * cc + 3] * scB));
           } else {
-            st_shared4(pb + swz128(rA, cc), pack_bf16(pr[4 * cc], pr[4 * cc + 1]));
-            st_shared4(pb + swz128(rB, cc), pack_bf16(pr[4 * cc + 2], pr[4 * cc + 3]));
+            st_shared4(pb + swz128(rA, cc + 4 * grp), pack_bf16(pr[4 * cc], pr[4 * cc + 1]));
+            st_shared4(pb + swz128(rB, cc + 4 * grp), pack_bf16(pr[4 * cc + 2], pr[4 * cc + 3]));
           }
         }
 #pragma unroll
-        for (int cc = 0; cc < 8; ++cc) {
+        for (int cc = 0; cc < NC / 8; ++cc) {
           l_part[2 * cc] += pr[4 * cc] + pr[4 * cc + 2];
           l_part[2 * cc + 1] += pr[4 * cc + 1] + pr[4 * cc + 3];
         }
@@ -1285,13 +1323,13 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           tc_fence_after();
           for (int tt = 0; tt < NT; ++tt) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < NC / 16; ++q) {
               float o[16];
-              const uint32_t ta = tmem + lane_base + kOCol + 64 * tt + 16 * q;
+              const uint32_t ta = tmem + lane_base + kOCol + 64 * tt + col0 + 16 * q;
               tmem_ld16(ta, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= bc_m[64 + 16 * q + i];
+              for (int i = 0; i < 16; ++i) o[i] *= bc_m[NC + 16 * q + i];
               tmem_st16(ta, o);
             }
           }
@@ -1303,22 +1341,22 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       }
       if (!ok) break;
       // ---------------- epilogue
-      // column sums over this warp's rows (lane l: columns 2 l, 2 l + 1), then over the 4 warps
-      float* red = s_red + (g & 1) * 256;
-      *reinterpret_cast<float2*>(red + warp * 64 + 2 * lane) = col_reduce16<false>(l_part, lane);
-      named_bar_sync(1, 128);
+      // column sums over this warp's rows, then over the 4 warps
+      float* red = s_red + (g & 1) * 256 + grp * 128;
+      reduce_columns(std::false_type(), l_part, red);
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = 2 * lane + j;
-        const float lt = red[col] + red[64 + col] + red[128 + col] + red[192 + col];
+      for (int j = 0; j < kOwn; ++j) {
+        const int col = col0 + own + j;
+        const float* r = red + own + j;
+        const float lt = r[0] + r[NC] + r[2 * NC] + r[3 * NC];
         // a paged call passes a NaN on (a visible row holds one) instead of dropping the range
         const bool some = PAGED ? lt != 0.f : lt > 0.f;
         const float lse_w = some ? (m_own[j] + log2f(lt)) * kLn2 : -CUDART_INF_F;
         float cw, cp = 0.f;
         if (EPI == EPI_PARTIAL) {
           cw = some ? 1.f / lt : 0.f;
-          if (warp == 0 && col < p.H) p.lse_part[item * p.H + col] = lse_w;
+          if (quad == 0 && col < p.H) p.lse_part[item * p.H + col] = lse_w;
         } else {
           const int64_t o = bt * p.H + (col < p.H ? col : 0);
           const float lse_p = (p.O_in && col < p.H) ? p.lse_in[o] : -CUDART_INF_F;
@@ -1330,8 +1368,8 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           cw = some ? ew / (den * lt) : 0.f;
           cp = den > 0.f ? ep / den : 0.f;
         }
-        bc_m[64 + col] = cw;
-        bc_m[128 + col] = cp;
+        bc_m[NC + own + j] = cw;
+        bc_m[2 * NC + own + j] = cp;
       }
       __syncwarp();
       const bool any = rs.c1 > rs.c0;
@@ -1353,14 +1391,14 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       // writes O = 0 for an empty row set)
       const int n_out_tiles = (EPI == EPI_PARTIAL && !any && (PAGED || p.per_item > 0)) ? 0 : NT;
       for (int tt = 0; tt < n_out_tiles; ++tt) {
-        float o[64];
+        float o[NC];
         if (any) {
-          tmem_ld32(tmem + lane_base + kOCol + 64 * tt, o);
-          tmem_ld32(tmem + lane_base + kOCol + 64 * tt + 32, o + 32);
+          tmem_ld32(tmem + lane_base + kOCol + 64 * tt + col0, o);
+          if (!kTwo) tmem_ld32(tmem + lane_base + kOCol + 64 * tt + 32, o + 32);
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) o[i] = 0.f;
+          for (int i = 0; i < NC; ++i) o[i] = 0.f;
         }
         if (any && tt == NT - 1) {
           tc_fence_before();
@@ -1368,11 +1406,11 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         }
         const int d = 128 * tt + e;
 #pragma unroll
-        for (int h = 0; h < 64; ++h) o[h] *= bc_m[64 + h];
+        for (int h = 0; h < NC; ++h) o[h] *= bc_m[NC + h];
         if (EPI == EPI_COMBINE && p.O_in) {
 #pragma unroll
-          for (int h = 0; h < 64; ++h)
-            if (h < p.H) o[h] = fmaf(bc_m[128 + h], __ldg(p.O_in + (obase + h) * D + d), o[h]);
+          for (int h = 0; h < NC; ++h)
+            if (col0 + h < p.H) o[h] = fmaf(bc_m[2 * NC + h], __ldg(p.O_in + (obase + col0 + h) * D + d), o[h]);
         }
         if (EPI == EPI_COMBINE && p.inv_rope && tt == NT - 1 && e >= 128 - p.rope_dim) {
           // inverse rotation by -pos: (a, b) -> (a cos + b sin, -a sin + b cos),
@@ -1380,38 +1418,38 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           const int half = p.rope_dim / 2;
           const int lr = e - (128 - p.rope_dim);            // 0 .. rope_dim - 1
 #pragma unroll
-          for (int h = 0; h < 64; ++h) xs[h * 64 + lr] = o[h];
+          for (int h = 0; h < NC; ++h) xs[h * 64 + lr] = o[h];
           named_bar_sync(3, 64);
           const bool first = lr < half;
           const int pl = first ? lr + half : lr - half;
           const float2 csj = cs[first ? lr : lr - half];
 #pragma unroll
-          for (int h = 0; h < 64; ++h) {
+          for (int h = 0; h < NC; ++h) {
             const float w = xs[h * 64 + pl];
             o[h] = first ? o[h] * csj.x + w * csj.y : o[h] * csj.x - w * csj.y;
           }
         }
         if (EPI == EPI_COMBINE) {
           if (p.out_bf16) {
-            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) + obase * D + d;
+            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) + (obase + col0) * D + d;
 #pragma unroll
-            for (int h = 0; h < 64; ++h)
-              if (h < p.H) dst[(int64_t)h * D] = __float2bfloat16_rn(o[h]);
+            for (int h = 0; h < NC; ++h)
+              if (col0 + h < p.H) dst[(int64_t)h * D] = __float2bfloat16_rn(o[h]);
           } else {
-            float* dst = reinterpret_cast<float*>(p.out) + obase * D + d;
+            float* dst = reinterpret_cast<float*>(p.out) + (obase + col0) * D + d;
 #pragma unroll
-            for (int h = 0; h < 64; ++h)
-              if (h < p.H) dst[(int64_t)h * D] = o[h];
+            for (int h = 0; h < NC; ++h)
+              if (col0 + h < p.H) dst[(int64_t)h * D] = o[h];
           }
         } else {
-          float* dst = p.O_part + obase * D + d;
+          float* dst = p.O_part + (obase + col0) * D + d;
 #pragma unroll
-          for (int h = 0; h < 64; ++h)
-            if (h < p.H) dst[(int64_t)h * D] = o[h];
+          for (int h = 0; h < NC; ++h)
+            if (col0 + h < p.H) dst[(int64_t)h * D] = o[h];
         }
       }
       ++icount;
-      named_bar_sync(1, 128);   // s_red / bc / exchange reuse across items
+      named_bar_sync(bar1, 128);   // s_red / bc / exchange reuse across items
     }
   }
   __syncwarp();                 // reconverge role warps before the CTA barrier
@@ -1803,7 +1841,7 @@ csa_status_t launch_paged(const AttnParams& p, const AttnMaps& m, cudaStream_t s
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
   const int grid = EPI == EPI_PARTIAL ? std::min(p.max_items, num_sms()) : (int)std::min<int64_t>(p.n_tok, num_sms());
-  e = launch_pdl(kern, dim3(grid), dim3(attn_threads<KV, true>()), smem, st, p, m.q, m.kv, m.tok);
+  e = launch_pdl(kern, dim3(grid), dim3(attn_threads<true>()), smem, st, p, m.q, m.kv, m.tok);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: launch failed: %s", cudaGetErrorString(e));
   return check_launch("csa_paged_attention");
 }
