@@ -43,6 +43,7 @@
 // chunks) are taken grid-stride, or, for split-KV calls with more items than
 // SMs, claimed from a counter so that ranges of unequal length balance.
 #include <algorithm>
+#include <climits>
 #include <cstring>
 #include <type_traits>
 #include <cuda_bf16.h>
@@ -125,7 +126,7 @@ struct AttnParams {
   int64_t n_tok;
   PageTable pt1, pt2;
   int max_items;                // > 0: the rows are cut into at most this many ranges (see SplitPlan)
-  int32_t* plan;                // [n_seq + 1] first range of each sequence, for the merge
+  int2* plan;                   // [n_tok] each token's first range and how many (0: left alone), for the merge
 };
 
 // Rows are consumed in half chunks of 64 (one ring slot each).  The window
@@ -158,17 +159,22 @@ __device__ __forceinline__ int count_valid_warp(const int32_t* row, int k, int l
   return s1;
 }
 
-// Whole-warp call: every lane gets the same row set.  `per_plan`: half chunks
-// per range of a paged call (0: the whole row set is one range).
+// Entries of ratio m that are complete at pos >= 0.
+__device__ __forceinline__ int64_t entries_at(int64_t pos, int m) {
+  return pos < INT_MAX ? (int64_t)(((uint32_t)pos + 1) / (uint32_t)m) : (pos + 1) / m;
+}
+// Whole-warp call: every lane gets the same row set.  A paged call's item has its
+// position and the half chunks of a range (per_plan; 0: the whole row set is one).
 template <bool PAGED = false>
-__device__ __forceinline__ RowSet row_set_warp(const AttnParams& p, int b, int t, int sp, int lane, int per_plan = 0) {
+__device__ __forceinline__ RowSet row_set_warp(const AttnParams& p, int b, int t, int sp, int lane, int per_plan = 0,
+                                               int64_t paged_pos = 0) {
   RowSet r{0, 0, 0, 0, 0, 0, 0, 0, nullptr};
-  const int64_t pos = (p.q_pos ? p.q_pos[b] : 0) + t;
+  const int64_t pos = PAGED ? paged_pos : (p.q_pos ? p.q_pos[b] : 0) + t;
   if (p.src1 == SRC1_GATHER) {
     r.idx = p.idx + ((int64_t)b * p.T + t) * p.k;
     r.n1 = count_valid_warp(r.idx, p.k, lane);
   } else if (p.src1 == SRC1_DENSE) {
-    r.n1 = PAGED ? (int)max((int64_t)0, min(p.cap, (pos + 1) / p.m)) : (int)min(p.cap, (pos + 1) / p.m);
+    r.n1 = (int)min(p.cap, PAGED ? entries_at(pos, p.m) : (pos + 1) / p.m);
   }
   if (p.src2 == SRC2_WINDOW) {
     // W = 0 (paged calls only): every row up to the position
@@ -194,7 +200,7 @@ __device__ __forceinline__ RowSet row_set_warp(const AttnParams& p, int b, int t
 // reaches the end of the table.
 __device__ __forceinline__ int paged_half_chunks(const AttnParams& p, int64_t pos0, int64_t pos1) {
   int64_t n1 = 0, n2 = 0;
-  if (p.src1 == SRC1_DENSE) n1 = max((int64_t)0, min(p.cap, (pos1 + 1) / p.m));
+  if (p.src1 == SRC1_DENSE) n1 = pos1 < 0 ? 0 : min(p.cap, entries_at(pos1, p.m));
   if (p.src2 == SRC2_WINDOW) {
     const int64_t pos = max(pos0, min(pos1, p.cap2 - 1));
     n2 = max((int64_t)0, min(p.cap2, pos + 1) - (p.W == 0 ? 0 : max((int64_t)0, pos - p.W + 1)));
@@ -205,59 +211,88 @@ __device__ __forceinline__ int paged_half_chunks(const AttnParams& p, int64_t po
 // Work items of a paged call with few query tokens.  Every row set is cut into
 // ranges of `per` half chunks; sequence b's tokens take ranges first[b] ..
 // first[b + 1] - 1, the same number each (that of its longest row set).  `per` is
-// the smallest step of the search below that leaves at most max_items ranges,
-// one for each SM, so that the call is one wave whatever the lengths are: they
-// are known on the device only.  Without empty ranges to step over, an item
-// costs a CTA nothing but its rows.  Whole-CTA call.
-constexpr int kPlanSeqs = 1024;    // sequences that the shared-memory plan holds
+// the smallest found that leaves at most max_items ranges, one for each SM, so that
+// the call is one wave whatever the lengths are: they are known on the device only.
+// Without empty ranges to step over, an item costs a CTA nothing but its rows.
+constexpr int kPlanSeqs = 384;     // sequences that the shared-memory plan holds
 struct SplitPlan {
+  int64_t pos[kPlanSeqs];          // q_pos
+  int32_t row[kPlanSeqs];          // first row of the batch
+  int32_t len[kPlanSeqs];          // tokens
+  int32_t ns[kPlanSeqs];           // half chunks of the longest row set, then a token's ranges
   int32_t first[kPlanSeqs + 1];
-  int32_t nh[kPlanSeqs];           // half chunks of the sequence's longest row set
-  int per;
+  int per[2];                      // of the two rounds of the search
 };
+// With n tokens (at most half of max_items) the ranges number less than
+// all / per + n, so per = all / (max_items - n), rounded up, is enough, and less than
+// all / max_items is not.  Every warp tries one value between; a second round tries
+// the values between the smallest that was enough and the one below.  Nothing of a
+// call runs before its plan, and the code is cold: the fewer instructions the
+// better, so the bounds are floats.  Whole-CTA call.
 __device__ __forceinline__ void make_plan(const AttnParams& p, SplitPlan& s, int tid, int nthreads) {
   for (int b = tid; b < p.n_seq; b += nthreads) {
     const int len = seq_len(p.cu_q, b, p.n_tok);
+    const int64_t pos = p.q_pos[b];
+    s.pos[b] = pos;
+    s.row[b] = p.cu_q[b];
+    s.len[b] = len;
     // a token without rows still has one (empty) range, which tells the merge so
-    s.nh[b] = len > 0 ? max(1, paged_half_chunks(p, p.q_pos[b], p.q_pos[b] + len - 1)) : 0;
-    s.first[b] = len;              // the lengths, until the prefix sums replace them
+    s.ns[b] = len > 0 ? max(1, paged_half_chunks(p, pos, pos + len - 1)) : 0;
   }
+  if (tid < 2) s.per[tid] = INT_MAX;
   __syncthreads();
-  if (tid < 32) {
-    auto sum = [&](int per) {      // per = 0: all half chunks; else the ranges
-      int64_t n = 0;
-      for (int b = tid; b < p.n_seq; b += 32)
-        n += (int64_t)s.first[b] * (per ? (s.nh[b] + per - 1) / per : s.nh[b]);
+  const int warp = tid >> 5, lane = tid & 31, warps = nthreads >> 5;
+  float all = 0.f;
+  uint32_t tokens = 0;
+  for (int b = lane; b < p.n_seq; b += 32) {
+    all += (float)s.len[b] * (float)s.ns[b];
+    tokens += s.len[b];
+  }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      return n;
-    };
-    const int64_t all = sum(0);
-    int64_t per = max((int64_t)1, (all + p.max_items - 1) / p.max_items);
-    // ends: from per = all on there is one range for each token, at most max_items
-    while (per < all && sum((int)per) > p.max_items) per += max((int64_t)1, per >> 4);
-    per = min(per, max((int64_t)1, all));
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  tokens = __reduce_add_sync(0xffffffffu, tokens);
+  uint32_t lo = max(1u, (uint32_t)(all / p.max_items));
+  uint32_t hi = lo + 1 + (uint32_t)(1.0001f * all / max(1, p.max_items - (int)tokens));
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    const uint32_t step = max(1u, (hi - lo + warps - 2) / (warps - 1));
+    const uint32_t per = min(hi, lo + step * warp);
+    uint32_t n = 0;
+    for (int b = lane; b < p.n_seq; b += 32) n += s.len[b] * (((uint32_t)s.ns[b] + per - 1) / per);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0 && (per == hi || n <= p.max_items)) atomicMin(&s.per[round], (int)per);
+    __syncthreads();
+    hi = s.per[round];
+    lo = max(lo, hi - min(hi, step - 1));
+  }
+  const uint32_t per = s.per[1];
+  if (warp == 0) {
     int at = 0;                    // exclusive prefix sums, 32 sequences a step
     for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
-      const int b = b0 + tid;
-      const int n = b < p.n_seq ? s.first[b] * (int)((s.nh[b] + per - 1) / per) : 0;
+      const int b = b0 + lane;
+      int n = 0;
+      if (b < p.n_seq) {
+        const int ns = ((uint32_t)s.ns[b] + per - 1) / per;
+        s.ns[b] = ns;
+        n = s.len[b] * ns;
+      }
       int inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (tid >= o) inc += v;
+        if (lane >= o) inc += v;
       }
       if (b < p.n_seq) s.first[b] = at + inc - n;
       at += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (tid == 0) { s.first[p.n_seq] = at; s.per = (int)per; }
+    if (lane == 0) s.first[p.n_seq] = at;
   }
   __syncthreads();
 }
 
 // Item -> sequence, token of the sequence, range, row of the batch.  False for
 // the rows of a paged call that are left alone: padding, negative positions.
-struct Item { int b, t, sp; int64_t bt; int per; };
+struct Item { int b, t, sp; int64_t bt; int per; int64_t pos; };
 template <bool PAGED>
 __device__ __forceinline__ bool locate_warp(const AttnParams& p, const SplitPlan* plan, int64_t item, int lane, Item& it) {
   if constexpr (PAGED) {
@@ -266,24 +301,27 @@ __device__ __forceinline__ bool locate_warp(const AttnParams& p, const SplitPlan
     if (plan) {
       it.b = find_seq_warp(plan->first, p.n_seq, item, lane);
       if (it.b < 0) return false;
-      const int f0 = plan->first[it.b], ns = (plan->first[it.b + 1] - f0) / seq_len(p.cu_q, it.b, p.n_tok);
-      it.t = (int)(item - f0) / ns;
-      it.sp = (int)(item - f0) % ns;
-      it.bt = p.cu_q[it.b] + it.t;
-      it.per = plan->per;
-      return p.q_pos[it.b] + it.t >= 0;
+      const uint32_t k = (uint32_t)item - plan->first[it.b], ns = plan->ns[it.b];
+      it.t = k / ns;
+      it.sp = k - it.t * ns;
+      it.bt = plan->row[it.b] + it.t;
+      it.per = plan->per[1];
+      it.pos = plan->pos[it.b] + it.t;
+      return it.pos >= 0 && (uint32_t)it.t < (uint32_t)plan->len[it.b];
     }
     it.bt = item;
     it.b = find_seq_warp(p.cu_q, p.n_seq, item, lane);
     if (it.b < 0) return false;
     it.t = (int)(item - p.cu_q[it.b]);
-    return p.q_pos[it.b] + it.t >= 0;
+    it.pos = p.q_pos[it.b] + it.t;
+    return it.pos >= 0;
   } else {
     it.bt = item / p.n_split;
     it.sp = (int)(item % p.n_split);
     it.b = (int)(it.bt / p.T);
     it.t = (int)(it.bt % p.T);
     it.per = 0;
+    it.pos = 0;
   }
   return true;
 }
@@ -534,8 +572,6 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
   if (PAGED && p.max_items > 0) {
     plan = reinterpret_cast<SplitPlan*>(s_abort + 1);
     make_plan(p, *plan, tid, blockDim.x);
-    if (blockIdx.x == 0)
-      for (int b = tid; b <= p.n_seq; b += blockDim.x) p.plan[b] = plan->first[b];
   }
   const int64_t n_items = !PAGED ? (int64_t)p.n_seq * p.T * p.n_split
                                  : plan ? min(plan->first[p.n_seq], p.max_items) : p.n_tok;
@@ -573,7 +609,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       if (!locate_warp<PAGED>(p, plan, item, lane, it)) continue;
       const int b = it.b, t = it.t;
       const int64_t bt = it.bt;
-      const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per);
+      const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per, it.pos);
       if (rs.c1 <= rs.c0) continue;
       // ---- Q tile: 64 rows x NS slabs of 128 B
       if (grp == 0 && !wait_bar<PAGED>(q_free, (qcount & 1) ^ 1, abort_flag)) { ok = false; break; }
@@ -1111,7 +1147,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       Item it;
       if (!locate_warp<PAGED>(p, plan, item, lane, it)) continue;
       const int b = it.b, t = it.t;
-      const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per);
+      const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per, it.pos);
       if (rs.c1 <= rs.c0) continue;
       if (PAGED || lane == 0) {
         if (role == 1) {
@@ -1164,6 +1200,20 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     const int rA = 16 * quad + (lane >> 2), rB = rA + 8;
     uint32_t g = 0, icount = 0;
     bool ok = true;
+    // each token's ranges, for the merge; these warps have nothing to do yet
+    if (PAGED && plan && blockIdx.x == 0 && warp < 4) {
+      for (int i = tid; i < p.n_tok; i += 128) {
+        int b = 0;                                       // the last sequence that starts at or before the token
+        for (int hi = p.n_seq; hi - b > 1;) {
+          const int mid = (b + hi) >> 1;
+          if (plan->row[mid] <= i) b = mid; else hi = mid;
+        }
+        const int t = i - plan->row[b], len = plan->len[b];
+        int2 r = make_int2(0, 0);
+        if (t >= 0 && t < len && plan->pos[b] + t >= 0) r = make_int2(plan->first[b] + t * plan->ns[b], plan->ns[b]);
+        p.plan[i] = r;
+      }
+    }
     // Maxima or sums of the columns over this warp's rows; red[w * NC + column] has
     // warp w's then, for all of the group.
     auto reduce_columns = [&](auto max, auto& v, float* red) {
@@ -1178,8 +1228,8 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       if (!locate_warp<PAGED>(p, plan, item, lane, it)) continue;
       const int b = it.b, t = it.t;
       const int64_t bt = it.bt;
-      const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per);
-      const int64_t pos = (p.q_pos ? p.q_pos[b] : 0) + t;
+      const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per, it.pos);
+      const int64_t pos = PAGED ? it.pos : (p.q_pos ? p.q_pos[b] : 0) + t;
       float2* cs = s_cs + (icount & 1) * 32;
       if (EPI == EPI_COMBINE && p.inv_rope && tid < 32) {
         // angle pos * inv_freq_j reduced to [0, 2 pi) in double (pos reaches 2^20
@@ -1578,25 +1628,20 @@ attn_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, co
 // one head of one token, 16 bytes a lane, four partials in flight; it skips
 // empty ranges, whose output was not written.
 __global__ void __launch_bounds__(128)
-paged_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, const int32_t* __restrict__ plan,
-                   const float* __restrict__ sink, const int32_t* __restrict__ cu_q, const int64_t* __restrict__ q_pos,
-                   int n_seq, int max_items, int H, int D, void* __restrict__ out, int out_bf16) {
+paged_merge_kernel(const float* Os, const float* Ls, const int2* plan, const float* sink, int max_items, int H, int D, void* out, int out_bf16) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int per_head = D / 128;
   const int h = unit / per_head, d = (unit % per_head) * 128 + 4 * lane;
   const int64_t bt = blockIdx.x;
-  const int b = find_seq_warp(cu_q, n_seq, bt, lane);
-  if (b < 0 || h >= H) return;
-  const int c0 = cu_q[b], f0 = plan[b];
-  if (q_pos[b] + (bt - c0) < 0) return;
-  const int ns = (plan[b + 1] - f0) / seq_len(cu_q, b, gridDim.x);
-  const int64_t i0 = f0 + (bt - c0) * ns;
-  if (i0 + ns > max_items) return;
-  const float sk = sink ? sink[h] : -CUDART_INF_F;
+  if (h >= H) return;
+  const int2 ranges = __ldcg(plan + bt);
+  const int i0 = ranges.x, ns = ranges.y;
+  if (ns <= 0 || i0 < 0 || i0 + ns > max_items) return;
+  const float sk = sink ? __ldcg(sink + h) : -CUDART_INF_F;
   float M = sk;
-  for (int i = lane; i < ns; i += 32) M = fmaxf(M, Ls[(i0 + i) * H + h]);
+  for (int i = lane; i < ns; i += 32) M = fmaxf(M, __ldcg(Ls + (int64_t)(i0 + i) * H + h));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (M == -CUDART_INF_F) M = 0.f;
@@ -1604,7 +1649,7 @@ paged_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, c
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < ns; s0 += 32) {
     const int s = s0 + lane;
-    const float e = s < ns ? __expf(Ls[(i0 + s) * H + h] - M) : 0.f;
+    const float e = s < ns ? __expf(__ldcg(Ls + (int64_t)(i0 + s) * H + h) - M) : 0.f;
     den += e;
     const int n = min(32, ns - s0);
     for (int j0 = 0; j0 < n; j0 += 4) {
@@ -1615,7 +1660,7 @@ paged_merge_kernel(const float* __restrict__ Os, const float* __restrict__ Ls, c
         c[u] = __shfl_sync(0xffffffffu, e, (j0 + u) & 31);
         const bool in = j0 + u < n && c[u] != 0.f;        // NaN reads too
         if (!in) c[u] = 0.f;
-        a[u] = in ? __ldg(reinterpret_cast<const float4*>(Os + ((i0 + s0 + j0 + u) * H + h) * D + d))
+        a[u] = in ? __ldcg(reinterpret_cast<const float4*>(Os + ((int64_t)(i0 + s0 + j0 + u) * H + h) * D + d))
                   : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
@@ -2112,8 +2157,8 @@ extern "C" size_t csa_paged_attention_workspace(int64_t n_tok, int n_seq, int H,
   if (n_tok <= 0 || n_seq <= 0 || H <= 0 || D <= 0) return 0;
   const size_t items = (size_t)paged_items(n_tok, n_seq);
   if (items == 0) return 0;
-  // the ranges' results, their lse, the first range of each sequence
-  return ((items * H * D * 4 + 255) / 256) * 256 + ((items * H * 4 + 255) / 256) * 256 + (((size_t)n_seq + 1) * 4 + 255) / 256 * 256;
+  // the ranges' results, their lse, the ranges of each token
+  return ((items * H * D * 4 + 255) / 256) * 256 + ((items * H * 4 + 255) / 256) * 256 + ((size_t)n_tok * 8 + 255) / 256 * 256;
 }
 
 extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H, int D, const int32_t* cu_q,
@@ -2208,12 +2253,12 @@ extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H,
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.O_part = reinterpret_cast<float*>(ws);
   p.lse_part = reinterpret_cast<float*>(ws + ((items * H * D * 4 + 255) / 256) * 256);
-  p.plan = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(p.lse_part) + ((items * H * 4 + 255) / 256) * 256);
+  p.plan = reinterpret_cast<int2*>(reinterpret_cast<uint8_t*>(p.lse_part) + ((items * H * 4 + 255) / 256) * 256);
   s = dispatch_paged<EPI_PARTIAL>(p, maps, D, kv_dtype, stream);
   if (s != CSA_OK) return s;
   cudaError_t le = launch_pdl(paged_merge_kernel, dim3((unsigned)n_tok, (unsigned)((H * (D / 128) + 3) / 4)), dim3(128), 0,
-                              stream, (const float*)p.O_part, (const float*)p.lse_part, (const int32_t*)p.plan, sink, cu_q,
-                              q_pos, n_seq, p.max_items, H, D, out, (int)p.out_bf16);
+                              stream, (const float*)p.O_part, (const float*)p.lse_part, (const int2*)p.plan, sink,
+                              p.max_items, H, D, out, (int)p.out_bf16);
   if (le != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention(merge): launch failed: %s", cudaGetErrorString(le));
   return check_launch("csa_paged_attention(merge)");
 }

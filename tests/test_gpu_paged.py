@@ -337,6 +337,8 @@ ATTN = [
     dict(lens=[2, 2], pos=[126, 511], H=64, D=512, m=128, W=None, sink=False),       # first entry at position 127
     dict(lens=[2, 2], pos=[126, 511], H=5, D=128, m=128, W=None, kind="e4m3", ps=32),
     dict(lens=[1] * 40, pos=[i * 37 for i in range(40)], H=4, D=128, W=1),
+    dict(lens=[0] * 600 + [1, 2], pos=[5] * 600 + [700, 90], H=8, D=128, W=0),
+    dict(lens=[0] * 250 + [1, 2] + [0] * 100, pos=[5] * 250 + [700, 90] + [9] * 100, H=64, D=512, W=0),
     # chunks: more tokens than ranges
     dict(lens=[70, 1, 0, 33], pos=[0, 500, 0, 131], H=64, D=512),
     dict(lens=[100], pos=[60], H=64, D=512, W=0),
