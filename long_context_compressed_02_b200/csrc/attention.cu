@@ -42,6 +42,16 @@
 // on a slab pair as soon as it lands.  Work items (query token, range of half
 // chunks) are taken grid-stride, or, for split-KV calls with more items than
 // SMs, claimed from a counter so that ranges of unequal length balance.
+//
+// Paged calls (PAGED: a ragged batch over caches in pages) run the same products.
+// A batch of few tokens is cut into one range for each SM by a plan that every CTA
+// makes from the lengths on the device, and the ranges are merged; MMAs are issued
+// by whole warps with one elected lane; rows are prefetched into L2 ahead of the
+// ring.  16 sequences, 64 heads x 512, 9,700 to 28,900 raw rows each: 80 us, of
+// which the rows at the copy rate are 50 us, the plan, the first loads and the
+// merge about 20.  32 sequences over 820 to 7,900 e4m3 entries and a window of 128:
+// 66 us (rows 14 us): the conversion of a half chunk takes its loaders 4,000 cycles
+// of mostly latency, two groups of them in turn.
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -72,7 +82,8 @@ constexpr int kThreads = 352;      // 11 warps: 4 softmax + epilogue, 4 loaders,
 // Paged calls have 4 more warps (11 - 14).  E4M3: a second group of loaders; the
 // groups take alternate half chunks, so one group's loads are in flight while the
 // other converts.  BF16: a second group for the softmax and the output, with
-// columns (heads) 32 .. 63, which it does to 0 .. 31 of the first (@@).
+// columns (heads) 32 .. 63 (3,500 tokens of 64 heads, window 128: 156 us against
+// 180 with one).
 template <bool PAGED>
 constexpr int attn_threads() { return PAGED ? kThreads + 128 : kThreads; }
 constexpr int kNQ = 64;            // query rows (heads) per tile = MMA N
@@ -845,7 +856,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           // as 2^-100: their rows' codes are worth nothing next to any RoPE part,
           // which must not overflow.  The pairs of slabs but the last take one rolled
           // loop, which loads one pair ahead: the code of all of them with their loads
-          // in flight at once missed the instruction caches (32 sequences of 512 to 8,192
+          // in flight at once missed the instruction caches (32 sequences of 820 to 7,900
           // entries: 76 us, 70 so).
           constexpr int kNope = D - 64;
           const int rl = lane & 15;
@@ -2210,15 +2221,16 @@ extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H,
   p.max_items = paged_items(n_tok, n_seq);
   // Chunks of several tokens a sequence share their rows on pairs of SMs, two of
   // 64 heads or more of fewer (group).  A pair's turn costs more than a token's here
-  // (3,300 tokens of 64 heads, window 128: 376 us against 211) and a row less
-  // (window 1024: 674 against 926); they meet at 512 rows a token (506 and 505), or
-  // fewer with more tokens to share them (16 heads, window 128: 110 against 203).
-  // How many rows the tokens see is known on the device only, so the rule goes by
-  // the most that the window and the tables allow.
+  // (3,500 tokens of 64 heads, window 128: 396 us against 171) and a row less than
+  // half (window 512: 506 against 451, 1024: 662 against 828); they meet at about 700
+  // rows a token.  With `group` times the tokens in a pair both its turn and its rows
+  // cost that much less, which the square follows (window 128, 32 heads: 210 against
+  // 160, 16 heads: 117 against 159).  How many rows the tokens see is known on the
+  // device only, so the rule goes by the most that the window and the tables allow.
   const int64_t lim = (int64_t)1 << 31;
   const int64_t group = std::max(1, 64 / H);
   const int64_t most = (tok_pages ? (W == 0 ? p.cap2 : std::min<int64_t>(W, p.cap2)) : 0) + (kv_pages ? p.cap : 0);
-  if (p.max_items == 0 && D == 512 && n_tok >= 2 * (int64_t)n_seq && kv_dtype == CSA_BF16 && most * group >= 512 &&
+  if (p.max_items == 0 && D == 512 && n_tok >= 2 * (int64_t)n_seq && kv_dtype == CSA_BF16 && most * group * group >= 704 &&
       (!tok_pages || (pair_page_size(tok_page_size) && n_tok_pages * tok_page_size < lim)) &&
       (!kv_pages || (pair_page_size(kv_page_size) && n_kv_pages * kv_page_size < lim))) {
     PairParams g{};

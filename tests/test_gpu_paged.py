@@ -485,6 +485,7 @@ def test_rows_behind_the_table_are_not_visible(csa):
 
 @pytest.mark.parametrize("lens,pos,H,D,W,cut", [([20], [250], 64, 512, 128, 256), ([20], [250], 8, 128, 128, 256),
                                                  ([20, 1], [200, 400], 64, 512, 0, 192), ([100], [1000], 64, 512, 600, 1024),
+                                                 ([100], [1000], 64, 512, 800, 1024),
                                                  ([100], [250], 8, 128, 128, 256)])
 def test_tokens_behind_the_table(csa, lens, pos, H, D, W, cut):
     """A window that reaches over the table's end shrinks from token to token."""
