@@ -494,7 +494,7 @@ csa_status_t csa_paged_append(const void* rows, csa_dtype_t in_dtype, int64_t ro
  * the tokens that see it mean nothing; rows behind max_pages * page_size are not
  * visible.  A visible row with a NaN or an infinity puts NaN into the result.
  * workspace: csa_paged_attention_workspace(n_tok, n_seq, H, D) bytes (0 from
- * about 75 tokens on), 16-byte aligned; calls sharing one must be ordered on
+ * about 75 tokens or 385 sequences on), 16-byte aligned; calls sharing one must be ordered on
  * one stream, and a captured graph keeps its own. */
 size_t csa_paged_attention_workspace(int64_t n_tok, int n_seq, int H, int D);
 csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H, int D, const int32_t* cu_q, const int64_t* q_pos,
