@@ -555,6 +555,61 @@ def test_two_graphs_replayed_with_new_positions(csa):
     csa.check_device_error()
 
 
+@pytest.mark.parametrize("kw", [dict(lens=[90, 60], pos=[700, 1500], H=64, D=512, W=0), dict(lens=[1, 2, 1], pos=[900, 40, 2000], H=64, D=512, W=0),
+                                dict(lens=[90, 1], pos=[600, 7], H=64, D=512, m=4, kind="e4m3"), dict(lens=[200], pos=[300], H=8, D=128)])
+def test_two_calls_at_once(csa, kw):
+    """Calls on two streams, back to back and overlapping, and a captured one replayed between them."""
+    cs = [Case(seed=s, **kw) for s in (1, 2)]
+    ref = [csa.csa_paged_attention(c.q, c.cu, c.qp, **c.kw) for c in cs]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        caught = csa.csa_paged_attention(cs[0].q, cs[0].cu, cs[0].qp, **cs[0].kw)
+    streams = [torch.cuda.Stream() for _ in cs]
+    got = [[], []]
+    for _ in range(8):
+        for i, (c, st) in enumerate(zip(cs, streams)):
+            got[i].append(csa.csa_paged_attention(c.q, c.cu, c.qp, stream=st, **c.kw))
+        g.replay()
+    torch.cuda.synchronize()
+    csa.check_device_error()
+    assert torch.equal(caught, ref[0])
+    assert all(torch.equal(o, ref[i]) for i in (0, 1) for o in got[i])
+
+
+def test_a_step_captured_as_one_graph(csa):
+    """The layer step in a graph, replayed as positions advance, equals the calls one by one."""
+    D, H, ps = 512, 64, 64
+    w, _ = csa.csa_rope_freqs(64)
+    g0 = torch.Generator(device="cuda").manual_seed(3)
+    tab = torch.arange(12, dtype=torch.int32, device="cuda").reshape(2, 6)
+    start = torch.randn(12, ps, D, generator=g0, device="cuda").to(BF)
+    cu, qp, n, _ = batch([1, 1], [100, 250])
+    q, rows = torch.empty(n, H, D, dtype=BF, device="cuda"), torch.empty(n, D, dtype=BF, device="cuda")
+    inputs = [(torch.randn(n, H, D, generator=g0, device="cuda").to(BF), torch.randn(n, D, generator=g0, device="cuda").to(BF)) for _ in range(4)]
+    pages = start.clone()
+    want = []
+    for k, (a, b) in enumerate(inputs):
+        want.append(csa.paged_layer_step(a, b, cu, qp + k, w, pages, tab, W=0))
+    held, pos = start.clone(), qp.clone()
+    q.copy_(inputs[0][0])
+    rows.copy_(inputs[0][1])
+    csa.paged_layer_step(q, rows, cu, pos, w, held.clone(), tab, W=0)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = csa.paged_layer_step(q, rows, cu, pos, w, held, tab, W=0)
+    for k, (a, b) in enumerate(inputs):
+        q.copy_(a)
+        rows.copy_(b)
+        pos.copy_(qp + k)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[k]), k
+    csa.check_device_error()
+    assert torch.equal(held, pages)
+
+
 def test_binding_refusals(csa):
     c = Case(lens=[2], pos=[10], H=8, D=128)
     x, w = c.q, csa.csa_rope_freqs(64)[0]
