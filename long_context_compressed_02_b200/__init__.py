@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -481,6 +482,8 @@ def _vector(what, name, g, n):
 
 def _like(what, t, dtype):
     """A new contiguous tensor of t's shape."""
+    if dtype is None and t.is_contiguous():
+        return torch.empty_like(t)
     if dtype is not None and dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise CsaError(f"{what}: out must be float32 or bfloat16")
     return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
@@ -671,6 +674,12 @@ def csa_paged_attention_workspace(n_tok, n_seq, H, D):
     return lib().csa_paged_attention_workspace(n_tok, n_seq, H, D)
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(dev, n_tok, n_seq, H, D):
+    """The size above for the current device `dev`: it follows from these alone."""
+    return csa_paged_attention_workspace(n_tok, n_seq, H, D)
+
+
 def csa_paged_attention(q, cu_q, q_pos, *, tok_pages=None, tok_table=None, W=128, kv_pages=None, kv_rope=None,
                         kv_scale=None, kv_table=None, m=128, sink=None, scale=None, out_dtype=None, out=None,
                         workspace=None, stream=None):
@@ -719,7 +728,7 @@ def csa_paged_attention(q, cu_q, q_pos, *, tok_pages=None, tok_table=None, W=128
         L = lib()
         ws_bytes = 0
         if workspace is None:
-            ws_bytes = L.csa_paged_attention_workspace(n, n_seq, H, D)
+            ws_bytes = _workspace_bytes(dev, n, n_seq, H, D)
             if ws_bytes:
                 workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
         else:
