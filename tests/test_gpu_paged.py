@@ -397,6 +397,46 @@ def test_attention_of_long_rows(csa, k):
     assert torch.equal(csa.csa_paged_attention(c.q, c.cu, c.qp, **c.kw)[:-1], out[:-1])
 
 
+@pytest.mark.parametrize("lens,pos,H,D", [([1, 2], [2000, 700], 64, 512), ([90], [1500], 16, 512), ([3], [900], 8, 128)])
+def test_e4m3_rows_as_stored(csa, lens, pos, H, D):
+    """Against the stored rows themselves.  The attention rounds their last 64 dims once more, relative to the
+    row's scale: by half(bf16) of each element, so a logit moves by at most e = half * scale * sum |q||r| over
+    those dims, every weight by a factor within exp(+-2 e), and the result by (half + 2 e) sum p |row|."""
+    c = Case(lens=lens, pos=pos, H=H, D=D, m=4, kind="e4m3", W=None, seed=9)
+    out = csa.csa_paged_attention(c.q, c.cu, c.qp, **c.kw)
+    csa.check_device_error()
+    codes = c.store[0].view(torch.float8_e4m3fn).double().numpy()
+    for i, b, p in c.toks[:3] + c.toks[-1:]:
+        ne = (p + 1) // 4
+        rows = np.concatenate([O.page_rows(codes, c.ktab[b], 0, ne) * O.page_rows(np64(c.store[2]), c.ktab[b], 0, ne)[:, None],
+                               O.page_rows(np64(c.store[1]), c.ktab[b], 0, ne)], -1)
+        q = np64(c.q[i])
+        ref, mag = O.paged_attention_row(q, rows, 1 / math.sqrt(D), np64(c.sink))
+        e = half(BF) / math.sqrt(D) * (np.abs(q[:, -64:]) @ np.abs(rows[:, -64:]).T).max(-1, keepdims=True)
+        tol = (2.0 ** -8 + 2.0 ** -9 + half(BF) + 2.02 * e) * mag + half(BF) * np.abs(ref)
+        assert np.all(np.abs(np64(out[i]) - ref) <= tol), (i, np.abs(np64(out[i]) - ref).max())
+
+
+@pytest.mark.parametrize("H,D,dims", [(64, 512, (0, 127, 128, 300, 384, 447)), (8, 128, (0, 37, 63))])
+def test_nan_codes_reach_the_tokens_that_see_them(csa, H, D, dims):
+    """A NaN code in any piece of an e4m3 row, and a NaN or an infinite scale."""
+    c = Case(lens=[40], pos=[360], H=H, D=D, m=4, kind="e4m3", W=None)
+    clean = csa.csa_paged_attention(c.q, c.cu, c.qp, **c.kw)
+    for row in (91, 95):                                      # complete at positions 367 and 383
+        first = 4 * row + 3 - 360
+        for d in dims + ("nan", "inf"):
+            codes, scale = c.kw["kv_pages"].clone(), c.kw["kv_scale"].clone()
+            at = int(c.ktab[0, row // 64]), row % 64
+            if isinstance(d, str):
+                scale[at] = float(d)
+            else:
+                codes[at][d] = 0xff if d % 2 else 0x7f
+            out = csa.csa_paged_attention(c.q, c.cu, c.qp, **dict(c.kw, kv_pages=codes, kv_scale=scale))
+            assert torch.equal(out[:first], clean[:first]), (row, d)
+            assert bool(torch.isnan(out[first:]).any(-1).all()), (row, d)
+    csa.check_device_error()
+
+
 def test_tokens_at_negative_positions_are_left_alone(csa):
     for lens, H, D in (([4], 64, 512), ([90], 64, 512), ([90], 8, 128)):
         c = Case(lens=lens, pos=[0], H=H, D=D, W=0)
