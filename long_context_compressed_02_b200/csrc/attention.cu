@@ -1232,7 +1232,14 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       else *reinterpret_cast<float2*>(red + quad * NC + own) = col_reduce16<decltype(max)::value>(v, lane);
       named_bar_sync(bar1, 128);
     };
-    for (uint32_t kk = 0; ok; ++kk) {
+    // Paged: after a wait that expired a warp only keeps its group's barriers, so that
+    // none waits for another for ever.
+    auto arrived = [&](uint64_t* bar, uint32_t parity) {
+      const bool r = wait_bar<PAGED>(bar, parity, abort_flag);
+      return PAGED ? __all_sync(0xffffffffu, r) != 0 : r;
+    };
+    auto keep_vote = [&] { if (named_bar_or(bar2, 128, false)) named_bar_sync(bar1, 128); };
+    for (uint32_t kk = 0; ok || PAGED; ++kk) {
       const int64_t item = get_item(kk, false);
       if (item >= n_items) break;
       Item it;
@@ -1259,9 +1266,13 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       float l_part[NC / 4];
 #pragma unroll
       for (int i = 0; i < NC / 4; ++i) l_part[i] = 0.f;
-      for (int c = rs.c0; c < rs.c1 && ok; ++c, ++g) {
+      for (int c = rs.c0; c < rs.c1 && (ok || PAGED); ++c, ++g) {
         const uint32_t sb = g & 1;
-        if (!wait_bar<PAGED>(&s_full[sb], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+        ok = ok && arrived(&s_full[sb], (g >> 1) & 1);
+        if (!ok) {
+          if (PAGED) keep_vote();
+          continue;
+        }
         tc_fence_after();
         float x[NC / 2], xb[NC / 2];
         if constexpr (kTwo) {
@@ -1283,7 +1294,11 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         float scA = 1.f, scB = 1.f;
         if (kCodes && !win) {
           // the scales came with the slot's last slab pair (complete: S was made from it)
-          if (!wait_bar<PAGED>(&kv_full[sb * NT + NT - 1], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+          ok = arrived(&kv_full[sb * NT + NT - 1], (g >> 1) & 1);
+          if (!ok) {
+            keep_vote();
+            continue;
+          }
           scA = s_scale[sb][rA];
           scB = s_scale[sb][rB];
 #pragma unroll
@@ -1359,7 +1374,8 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         }
         // P^T rows rA, rB -> this half chunk's buffer (MN-major B operand of PV),
         // free once PV(g - 2) has retired
-        if (!wait_bar<PAGED>(&pv_done[sb * NT + NT - 1], ((g >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+        ok = arrived(&pv_done[sb * NT + NT - 1], ((g >> 1) & 1) ^ 1);
+        if (!ok) continue;
         const uint32_t pb = smem_u32(sP + sb * kPBuf) + 4 * (lane & 3);
 #pragma unroll
         for (int cc = 0; cc < NC / 8; ++cc) {
@@ -1380,7 +1396,8 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           // O^T columns scale by alpha once PV(g - 1) has retired (this thread is
           // TMEM lane e of every tile)
           const uint32_t gp = g - 1;
-          if (!wait_bar<PAGED>(&pv_done[(gp & 1) * NT + NT - 1], (gp >> 1) & 1, abort_flag)) { ok = false; break; }
+          ok = arrived(&pv_done[(gp & 1) * NT + NT - 1], (gp >> 1) & 1);
+          if (!ok) continue;
           tc_fence_after();
           for (int tt = 0; tt < NT; ++tt) {
 #pragma unroll
@@ -1400,7 +1417,12 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
         fence_proxy_async_smem();
         mbar_arrive(&p_full[sb]);
       }
-      if (!ok) break;
+      if (!ok) {
+        if (!PAGED) break;
+        named_bar_sync(bar1, 128);
+        named_bar_sync(bar1, 128);
+        continue;
+      }
       // ---------------- epilogue
       // column sums over this warp's rows, then over the 4 warps
       float* red = s_red + (g & 1) * 256 + grp * 128;
@@ -1436,7 +1458,12 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       const bool any = rs.c1 > rs.c0;
       if (any) {
         const uint32_t gl = g - 1;               // last half chunk of this item
-        if (!wait_bar<PAGED>(&pv_done[(gl & 1) * NT + NT - 1], (gl >> 1) & 1, abort_flag)) { ok = false; break; }
+        ok = arrived(&pv_done[(gl & 1) * NT + NT - 1], (gl >> 1) & 1);
+        if (!ok) {
+          if (!PAGED) break;
+          named_bar_sync(bar1, 128);
+          continue;
+        }
         tc_fence_after();
       }
       // Each thread is TMEM lane e of every O^T tile, i.e. output dim d = 128 tt + e
