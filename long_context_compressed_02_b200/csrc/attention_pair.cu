@@ -315,24 +315,41 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
   uint8_t* sP = sQ + 8 * kSlab;                              // [4 slabs][64 rows][128 B]
   uint8_t* sK = sP + 4 * kSlab;
   uint8_t* sV = sK + kStages * kStage;
-  // Barriers.  A wait tells two neighbouring phases apart, no more, so each is
-  // waited on by roles that see all of its phases.
-  uint64_t* full_k = reinterpret_cast<uint64_t*>(sV + kStages * kStage);   // CTA 0: the parts of both CTAs are there
+  // Barriers.  A wait tells two neighbouring phases apart, no more: each is waited
+  // on by roles that see all of its phases, and none can complete its next phase
+  // before all of them have waited for the present one.  What holds it back stands
+  // with each.
+  // CTA 0: the parts of both CTAs are there.  The stage is loaded again after empty_k /
+  // empty_v, which the products issued behind this wait commit.
+  uint64_t* full_k = reinterpret_cast<uint64_t*>(sV + kStages * kStage);
   uint64_t* full_v = full_k + kStages;
-  uint64_t* empty_k = full_v + kStages;                      // the MMAs that read the stage are done
+  // The MMAs that read the stage are done.  Its next products need what its producer
+  // loads behind this wait (full_*: both CTAs').
+  uint64_t* empty_k = full_v + kStages;
   uint64_t* empty_v = empty_k + kStages;
-  uint64_t* patch = empty_v + kStages;                       // this CTA's part of the V stage is there, to be patched
-  uint64_t* q_full = patch + kStages;                           // CTA 0: the queries of both CTAs
-  uint64_t* q_free = q_full + 1;                             // the S products of an item are done
-  uint64_t* o_free = q_free + 1;                             // CTA 0: an item's output is out of TMEM in both CTAs
-  uint64_t* w_full = o_free + 1;                             // [4] an item is in s_work ...
-  uint64_t* w_free = w_full + kItems;                        // [4] ... and every warp has read it
-  uint64_t* s_full = w_free + kItems;                        // [2]
-  uint64_t* s_free = s_full + 2;                             // [2] CTA 0: read by the softmax of both CTAs
-  uint64_t* p_full = s_free + 2;                             // CTA 0: P and the rescaled O of both CTAs
-  uint64_t* pv_done = p_full + 1;
-  uint64_t* pv_sent = pv_done + 1;                           // CTA 0: the MMAs of a PV are issued
-  float* s_x = reinterpret_cast<float*>(pv_sent + 1);        // [2][4][64] maxima / sums of the row quarters
+  // This CTA's part of the V stage is there, to be patched.  The stage is loaded again
+  // after empty_v, and full_v needs the patch.
+  uint64_t* patch = empty_v + kStages;
+  uint64_t* q_full = patch + kStages;                        // CTA 0: the queries of both CTAs; loaded again after q_free
+  uint64_t* q_free = q_full + 1;                             // the S products of an item are done; the next need q_full of both CTAs
+  // CTA 0: an item's output is out of TMEM in both CTAs.  There is no other output
+  // before the PV products issued behind this wait.
+  uint64_t* o_free = q_free + 1;
+  uint64_t* w_full = o_free + 1;                             // [4] an item is in s_work; the slot is filled again after w_free
+  uint64_t* w_free = w_full + kItems;                        // [4] ... and every warp has read it; it is read again after w_full
+  // [2] the logits of every other tile; made again after s_free, which all warps that
+  // wait here arrive on
+  uint64_t* s_full = w_free + kItems;
+  uint64_t* s_free = s_full + 2;                             // [2] CTA 0: read by the softmax of both CTAs; read again after s_full
+  // CTA 0: P and the rescaled O of both CTAs.  The next tile's follow pv_done, by the
+  // wait before them or at the end of the item before.
+  uint64_t* p_full = s_free + 2;
+  uint64_t* pv_done = p_full + 1;                            // a tile's PV is done; the next needs p_full from all that wait here
+  // [2] CTA 0: the MMAs of every other tile's PV are issued.  S(t) waits for PV(t - 2),
+  // and the same barrier's PV(t) needs S(t).  One barrier for all tiles would not do:
+  // PV(t - 1) does not need S(t) and may be issued before it looks.
+  uint64_t* pv_sent = pv_done + 1;
+  float* s_x = reinterpret_cast<float*>(pv_sent + 2);        // [2][4][64] maxima / sums of the row quarters
   Work* s_work = reinterpret_cast<Work*>(s_x + 512);         // [4]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_work + kItems);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
@@ -347,8 +364,8 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
     }
     for (int i = 0; i < kItems; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_free[i], 14); }
     mbar_init(q_full, 2); mbar_init(q_free, 1); mbar_init(o_free, 16);
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 16); }
-    mbar_init(p_full, 16); mbar_init(pv_done, 1); mbar_init(pv_sent, 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 16); mbar_init(&pv_sent[i], 1); }
+    mbar_init(p_full, 16); mbar_init(pv_done, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
@@ -553,7 +570,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
     Stream x;
     for (; advance(x, 0, 0); ++t) {
       if (ok && x.i == 0) ok = wait_warp(q_full, (x.items & 1) ^ 1, abort_flag);
-      ok = ok && (t < 2 || wait_warp(pv_sent, t & 1, abort_flag));       // behind PV(t - 2)
+      ok = ok && wait_warp(&pv_sent[t & 1], ((t >> 1) & 1) ^ 1, abort_flag);       // behind PV(t - 2)
       ok = ok && wait_warp(&s_free[t & 1], ((t >> 1) & 1) ^ 1, abort_flag);
       if (!ok) continue;
 #pragma unroll 1
@@ -599,7 +616,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
                    (x.i | (v >> 1) | m) != 0);
         commit_pair(&empty_v[sl]);
       }
-      if (lane == 0) mbar_arrive(pv_sent);
+      if (lane == 0) mbar_arrive(&pv_sent[t & 1]);
       if (ok) commit_pair(pv_done);
     }
   } else {
@@ -839,7 +856,7 @@ csa_status_t launch_paged_pair(PairParams& p, cudaStream_t st) {
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return fail(CSA_ERR_CUDA, "csa_paged_attention: cuTensorMapEncodeTiled (pages) failed");
   }
-  const size_t smem = 12 * kSlab + 2 * kStages * kStage + (5 * kStages + 10 + 2 * kItems) * 8 + 512 * 4 + kItems * sizeof(Work) + 16;
+  const size_t smem = 12 * kSlab + 2 * kStages * kStage + (5 * kStages + 11 + 2 * kItems) * 8 + 512 * 4 + kItems * sizeof(Work) + 16;
   cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return fail(CSA_ERR_CUDA, "csa_paged_attention: cannot reserve %zu bytes of shared memory: %s", smem, cudaGetErrorString(e));
   // Every sequence's last tile may be partly filled: an upper bound of the tiles
