@@ -497,6 +497,14 @@ csa_status_t csa_paged_append(const void* rows, csa_dtype_t in_dtype, int64_t ro
  * about 75 tokens or 385 sequences on), 16-byte aligned; calls sharing one must be ordered on
  * one stream, and a captured graph keeps its own. */
 size_t csa_paged_attention_workspace(int64_t n_tok, int n_seq, int H, int D);
+/* 1 if a call with these sizes works on pairs of SMs that share their rows, 0 if a
+ * token at a time (max_pages 0: no such cache).  The two round differently, and the
+ * choice goes by the most rows that W and the tables allow: a wider table, unused
+ * columns included, can change a result's last bits and a call's time.  No device call but
+ * for the number of SMs. */
+int csa_paged_attention_pairs(int64_t n_tok, int n_seq, int H, int D, int tok_max_pages, int64_t n_tok_pages,
+                              int tok_page_size, int W, csa_dtype_t kv_dtype, int kv_max_pages, int64_t n_kv_pages,
+                              int kv_page_size);
 csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H, int D, const int32_t* cu_q, const int64_t* q_pos,
                                  int n_seq, const void* tok_pages, const int32_t* tok_table, int tok_max_pages,
                                  int64_t n_tok_pages, int tok_page_size, int W, const void* kv_pages,

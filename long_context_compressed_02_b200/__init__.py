@@ -80,6 +80,7 @@ def lib():
                               P, I64, I64, I, P], I),
         "csa_paged_append": ([P, I, I64, I64, I, P, P, I, P, I, I, I64, I, P, F, P, I, I, F, P, I, P, P, P], I),
         "csa_paged_attention_workspace": ([I64, I, I, I], SZ),
+        "csa_paged_attention_pairs": ([I64, I, I, I, I, I64, I, I, I, I, I64, I], I),
         "csa_paged_attention": ([P, I64, I, I, P, P, I, P, P, I, I64, I, I, P, I, P, P, P, I, I64, I, I, P, F, P, SZ, P,
                                  I, P], I),
         "csa_index_topk_fp4": ([P, P, P, P, P, P, I, I, I, I64, I, I, P, P, SZ, P], I),
@@ -672,6 +673,16 @@ def csa_paged_append(rows, cu_q, q_pos, block_table, pages, inv_freq, *, pages_r
 
 def csa_paged_attention_workspace(n_tok, n_seq, H, D):
     return lib().csa_paged_attention_workspace(n_tok, n_seq, H, D)
+
+
+def csa_paged_attention_pairs(q, q_pos, *, tok_pages=None, tok_table=None, W=128, kv_pages=None, kv_table=None):
+    """Whether csa_paged_attention, called with these, works on pairs of SMs (True)
+    or a token at a time; the two round differently.  Shapes and dtypes alone are read."""
+    n, H, D = q.shape
+    tok = (0, 0, 1) if tok_pages is None else (tok_table.shape[1], *tok_pages.shape[:2])
+    kv = (0, 0, 1) if kv_pages is None else (kv_table.shape[1], *kv_pages.shape[:2])
+    return bool(lib().csa_paged_attention_pairs(n, q_pos.shape[0], H, D, *tok, W,
+                                                BF16 if kv_pages is None else _DT[kv_pages.dtype], *kv))
 
 
 @functools.lru_cache(maxsize=4096)

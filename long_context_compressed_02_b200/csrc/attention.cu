@@ -2177,6 +2177,26 @@ int paged_items(int64_t n_tok, int n_seq) {
   return n_tok * 2 <= sms && n_seq <= kPlanSeqs ? sms : 0;
 }
 
+// Whether a call's tokens go to the pair kernel.  Chunks of several tokens a sequence
+// share their rows on pairs of SMs, two of 64 heads or more of fewer (group).  A
+// pair's turn costs more than a token's here (3,500 tokens of 64 heads, window 128:
+// 396 us against 171) and a row less than half (window 512: 506 against 451, 1024:
+// 662 against 828); they meet at about 700 rows a token.  With `group` times the
+// tokens in a pair both its turn and its rows cost that much less, which the square
+// follows (window 128, 32 heads: 210 against 160, 16 heads: 117 against 159).  How
+// many rows the tokens see is known on the device only, so the rule goes by the most
+// that the window and the tables allow.  A cache that the call has not has cap 0
+// (rows that a sequence's table names) and no rows.
+bool takes_pairs(int64_t n_tok, int n_seq, int H, int D, int64_t tok_cap, int64_t tok_rows, int tok_page_size, int W,
+                 csa_dtype_t kv_dtype, int64_t kv_cap, int64_t kv_rows, int kv_page_size) {
+  const int64_t lim = (int64_t)1 << 31;
+  const int64_t group = std::max(1, 64 / H);
+  const int64_t most = (W == 0 ? tok_cap : std::min<int64_t>(W, tok_cap)) + kv_cap;
+  return D == 512 && n_tok >= 2 * (int64_t)n_seq && kv_dtype == CSA_BF16 && most * group * group >= 704 &&
+         (tok_cap == 0 || (pair_page_size(tok_page_size) && tok_rows < lim)) &&
+         (kv_cap == 0 || (pair_page_size(kv_page_size) && kv_rows < lim)) && paged_items(n_tok, n_seq) == 0;
+}
+
 csa_status_t check_pages(const char* what, const void* pages, const int32_t* table, int max_pages, int64_t n_pages,
                          int page_size) {
   CSA_REQUIRE(aligned16(pages), "csa_paged_attention: %s pages must be 16-byte aligned", what);
@@ -2197,6 +2217,16 @@ extern "C" size_t csa_paged_attention_workspace(int64_t n_tok, int n_seq, int H,
   if (items == 0) return 0;
   // the ranges' results, their lse, the ranges of each token
   return ((items * H * D * 4 + 255) / 256) * 256 + ((items * H * 4 + 255) / 256) * 256 + ((size_t)n_tok * 8 + 255) / 256 * 256;
+}
+
+extern "C" int csa_paged_attention_pairs(int64_t n_tok, int n_seq, int H, int D, int tok_max_pages, int64_t n_tok_pages,
+                                         int tok_page_size, int W, csa_dtype_t kv_dtype, int kv_max_pages,
+                                         int64_t n_kv_pages, int kv_page_size) {
+  if (n_tok <= 0 || n_seq <= 0 || H < 1 || H > 64) return 0;
+  const bool tok = tok_max_pages > 0, kv = kv_max_pages > 0;
+  return takes_pairs(n_tok, n_seq, H, D, tok ? (int64_t)tok_max_pages * tok_page_size : 0, tok ? n_tok_pages * tok_page_size : 0,
+                     tok_page_size, W, kv ? kv_dtype : CSA_BF16, kv ? (int64_t)kv_max_pages * kv_page_size : 0,
+                     kv ? n_kv_pages * kv_page_size : 0, kv_page_size);
 }
 
 extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H, int D, const int32_t* cu_q,
@@ -2246,20 +2276,8 @@ extern "C" csa_status_t csa_paged_attention(const void* q, int64_t n_tok, int H,
   p.scale = scale; p.scale_log2 = scale * 1.4426950408889634f;
   p.sink = sink; p.out = out; p.out_bf16 = out_dtype == CSA_BF16;
   p.max_items = paged_items(n_tok, n_seq);
-  // Chunks of several tokens a sequence share their rows on pairs of SMs, two of
-  // 64 heads or more of fewer (group).  A pair's turn costs more than a token's here
-  // (3,500 tokens of 64 heads, window 128: 396 us against 171) and a row less than
-  // half (window 512: 506 against 451, 1024: 662 against 828); they meet at about 700
-  // rows a token.  With `group` times the tokens in a pair both its turn and its rows
-  // cost that much less, which the square follows (window 128, 32 heads: 210 against
-  // 160, 16 heads: 117 against 159).  How many rows the tokens see is known on the
-  // device only, so the rule goes by the most that the window and the tables allow.
-  const int64_t lim = (int64_t)1 << 31;
-  const int64_t group = std::max(1, 64 / H);
-  const int64_t most = (tok_pages ? (W == 0 ? p.cap2 : std::min<int64_t>(W, p.cap2)) : 0) + (kv_pages ? p.cap : 0);
-  if (p.max_items == 0 && D == 512 && n_tok >= 2 * (int64_t)n_seq && kv_dtype == CSA_BF16 && most * group * group >= 704 &&
-      (!tok_pages || (pair_page_size(tok_page_size) && n_tok_pages * tok_page_size < lim)) &&
-      (!kv_pages || (pair_page_size(kv_page_size) && n_kv_pages * kv_page_size < lim))) {
+  if (takes_pairs(n_tok, n_seq, H, D, tok_pages ? p.cap2 : 0, tok_pages ? n_tok_pages * tok_page_size : 0, tok_page_size, W,
+                  kv_dtype, kv_pages ? p.cap : 0, kv_pages ? n_kv_pages * kv_page_size : 0, kv_page_size)) {
     PairParams g{};
     g.q = q; g.cu_q = cu_q; g.q_pos = q_pos; g.n_seq = n_seq; g.H = H; g.n_tok = n_tok;
     g.rows[0] = tok_pages; g.pt[0] = p.pt2; g.cap[0] = p.cap2; g.W = W;

@@ -191,3 +191,29 @@ def test_oracle_attention_of_no_rows_is_zero():
     assert not out.any() and not mag.any()
     out, _ = O.paged_attention_row(np.ones((2, 8)), np.ones((1, 8)), 1.0, np.array([8.0, -math.inf]))
     assert np.allclose(out[0], 0.5) and np.allclose(out[1], 1.0)
+
+
+def _pairs(n, n_seq, H, D, W, tok_rows, *, ps=64, kv_rows=0, kv=torch.bfloat16, kv_ps=64):
+    m = dict(device="meta")
+    q, pos = torch.empty(n, H, D, dtype=torch.bfloat16, **m), torch.empty(n_seq, dtype=torch.int64, **m)
+    kw = {}
+    if tok_rows:
+        kw.update(tok_pages=torch.empty(9, ps, D, dtype=torch.bfloat16, **m), tok_table=torch.empty(n_seq, tok_rows // ps, **m))
+    if kv_rows:
+        kw.update(kv_pages=torch.empty(9, kv_ps, D, dtype=kv, **m), kv_table=torch.empty(n_seq, kv_rows // kv_ps, **m))
+    return csa.csa_paged_attention_pairs(q, pos, W=W, **kw)
+
+
+def test_which_calls_work_on_pairs(L):
+    """Chunks of at least two tokens a sequence on average, and 704 rows a token that window and tables allow,
+    fewer with the square of the tokens that a pair holds."""
+    assert _pairs(100, 1, 64, 512, 0, 704) and not _pairs(100, 1, 64, 512, 0, 640)
+    assert _pairs(100, 50, 64, 512, 0, 704) and not _pairs(100, 51, 64, 512, 0, 704)
+    assert not _pairs(74, 1, 64, 512, 0, 4096) and _pairs(75, 1, 64, 512, 0, 4096)       # split over the SMs
+    assert not _pairs(100, 1, 64, 128, 0, 4096)
+    assert _pairs(100, 1, 64, 512, 704, 1024) and not _pairs(100, 1, 64, 512, 703, 1024)
+    assert _pairs(100, 1, 32, 512, 176, 1024) and not _pairs(100, 1, 32, 512, 175, 1024)
+    assert _pairs(100, 1, 64, 512, 64, 1024, kv_rows=640) and not _pairs(100, 1, 64, 512, 63, 1024, kv_rows=640)
+    assert _pairs(100, 1, 64, 512, 0, 0, kv_rows=704) and not _pairs(100, 1, 64, 512, 0, 704, kv_rows=64, kv=torch.uint8)
+    assert not _pairs(100, 1, 64, 512, 0, 4096, ps=8) and not _pairs(100, 1, 64, 512, 0, 4096, kv_rows=64, kv_ps=8)
+    assert L.csa_paged_attention_pairs(0, 0, 64, 512, 64, 9, 64, 0, 1, 0, 0, 1) == 0
