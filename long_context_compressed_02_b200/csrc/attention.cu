@@ -339,7 +339,10 @@ __device__ __forceinline__ bool locate_warp(const AttnParams& p, const SplitPlan
 
 // mbarrier.try_wait suspends the thread in hardware until the phase completes
 // (or a short system time limit passes), so the loop needs no sleep of its own;
-// the wall clock and the CTA's abort flag are checked every 64 polls.
+// the wall clock and the CTA's abort flag are checked every 64 polls.  Only the
+// first try is inlined, and the loops around the loads' waits are not unrolled: the
+// roles' code misses the instruction caches, and a small call runs most of it once
+// (mixed decode stack 600 us with both written out, 586 so).
 __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   uint64_t start = 0;
   for (uint32_t i = 1;; ++i) {
@@ -355,24 +358,8 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
   atomicOr(&g_err_attn, DEV_ERR_TIMEOUT_MBAR);
   return false;
 }
-// SHORT: only the first try inlined, for the paged form, whose roles' code misses
-// the instruction caches.
-template <bool SHORT = false>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if constexpr (SHORT) return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag);
-  uint64_t start = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort_flag) return false;
-      const uint64_t now = global_ns();
-      if (start == 0) start = now;
-      else if (now - start > kWaitNs) break;
-    }
-  }
-  *abort_flag = 1;
-  atomicOr(&g_err_attn, DEV_ERR_TIMEOUT_MBAR);
-  return false;
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag);
 }
 
 // 2^x on the SFU (flush-to-zero: results below 2^-126 become 0, which only
@@ -551,7 +538,6 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
   int64_t* s_items = reinterpret_cast<int64_t*>(item_empty + 4);   // [4]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_items + 4);
   int* s_abort = reinterpret_cast<int*>(s_tmem + 1);
-  constexpr int kRoll = PAGED ? 1 : D / 128;         // unrolling of the loads' loops, see wait_bar
   constexpr bool kCodes = PAGED && KV == KV_FP8;     // slots hold e4m3 codes, row scales apart
   constexpr bool kTwo = PAGED && !kCodes;            // two groups of softmax warps, 32 columns each
   constexpr int kSoft = kTwo ? 256 : 128;            // their threads
@@ -594,18 +580,22 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     if (p.item_counter == nullptr) return (int64_t)blockIdx.x + (int64_t)k * gridDim.x;
     const uint32_t slot = k & 3, par = (k >> 2) & 1;
     if (fetcher) {
-      if (wait_bar<PAGED>(&item_empty[slot], par ^ 1, abort_flag)) s_items[slot] = (int64_t)atomicAdd(p.item_counter, 1u);
+      if (wait_bar(&item_empty[slot], par ^ 1, abort_flag)) s_items[slot] = (int64_t)atomicAdd(p.item_counter, 1u);
       else s_items[slot] = n_items;
       mbar_arrive(&item_full[slot]);
     }
     int64_t it = n_items;
-    if (wait_bar<PAGED>(&item_full[slot], par, abort_flag)) it = s_items[slot];
+    if (wait_bar(&item_full[slot], par, abort_flag)) it = s_items[slot];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&item_empty[slot]);
     return it;
   };
 
-  if ((warp >= 4 && warp < 8) || (kCodes && warp >= 11)) {
+  // Warps from 11 on, where there are any, load or share the softmax.  The loaders are
+  // "all others" for dense calls too: with 4 .. 7 alone the compiler lays the roles
+  // out so that the gathered decode attention (16 tokens, 512 entries and a window of
+  // 128) takes 38 us, 32 so.
+  if ((warp >= 4 && warp < 8) || (!kTwo && warp >= 11)) {
     // ============================ loaders
     const int grp = warp >= 11 ? 1 : 0;
     const int lt = grp ? tid - 352 : tid - 128;   // 0..127 of the group
@@ -623,7 +613,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
       const RowSet rs = row_set_warp<PAGED>(p, b, t, it.sp, lane, it.per, it.pos);
       if (rs.c1 <= rs.c0) continue;
       // ---- Q tile: 64 rows x NS slabs of 128 B
-      if (grp == 0 && !wait_bar<PAGED>(q_free, (qcount & 1) ^ 1, abort_flag)) { ok = false; break; }
+      if (grp == 0 && !wait_bar(q_free, (qcount & 1) ^ 1, abort_flag)) { ok = false; break; }
       ++qcount;
       if (grp != 0) {
         // the first group's
@@ -783,9 +773,9 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
                    : (int32_t)((int64_t)b * p.cap + (int64_t)cl * kRows);
         }
         if (tma) {
-#pragma unroll kRoll
+#pragma unroll 1
           for (int tt = 0; tt < NT; ++tt) {
-            if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
+            if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
             if (lt == 0) {
               mbar_expect_tx(&full[tt], 2 * kSlab);
               if constexpr (PAGED) {
@@ -829,9 +819,9 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           // Slab pair tt is signalled once this thread's copies of it have landed
           // (cp.async group tt), fenced to the async proxy here, on the producer
           // side, so the MMA issuer needs no proxy fence of its own.
-#pragma unroll kRoll
+#pragma unroll 1
           for (int tt = 0; tt < NT; ++tt) {
-            if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
+            if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
             gather16_bf16(rp, valid, 2 * tt, sl_base + (2 * tt) * kSlab, 16 * lw, lane);
             gather16_bf16(rp, valid, 2 * tt + 1, sl_base + (2 * tt + 1) * kSlab, 16 * lw, lane);
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -895,7 +885,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 next[i] = at[i] ? __ldg(reinterpret_cast<const uint4*>(at[i] + 128 * (tt + 1))) : zero;
-            if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
+            if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
             uint8_t* dst = sl_base + (2 * tt + odd) * kSlab;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -910,7 +900,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
             fence_proxy_async_smem();
             mbar_arrive(&full[tt]);
           }
-          if (!ok || !wait_bar<PAGED>(&done[NT - 1], fpar, abort_flag)) { ok = false; break; }
+          if (!ok || !wait_bar(&done[NT - 1], fpar, abort_flag)) { ok = false; break; }
           uint8_t* dst = sl_base + (NS - 2) * kSlab;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -1025,7 +1015,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
           for (int i = 0; i < 2; ++i) sc2[i] = __shfl_sync(0xffffffffu, sc, 8 * i + (lane >> 2));
 #pragma unroll
           for (int tt = 0; tt < NT; ++tt) {
-            if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
+            if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
             if (tt < NT - 1) {
               // piece l & 7 of the pair: slab 2 tt + (l & 7) / 4, 16-byte chunks 2 (l & 3), 2 (l & 3) + 1
               uint8_t* dst = sl_base + (2 * tt + ((lane & 7) >> 2)) * kSlab;
@@ -1081,7 +1071,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
             const float4 a = valid ? __ldg(reinterpret_cast<const float4*>(src + 64 * s) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
             v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
           }
-          if (!wait_bar<PAGED>(&done[tt], fpar, abort_flag)) { ok = false; break; }
+          if (!wait_bar(&done[tt], fpar, abort_flag)) { ok = false; break; }
           store_row_slab_f32(sl_base + s * kSlab, my_r, v);
           fence_proxy_async_smem();
           mbar_arrive(&full[tt]);
@@ -1100,7 +1090,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     // Paged calls issue from whole warps, the instruction alone predicated on one
     // elected lane: in convergent code the descriptors stay in uniform registers.
     auto wait_issuer = [&](uint64_t* bar, uint32_t parity) {
-      const bool r = wait_bar<PAGED>(bar, parity, abort_flag);
+      const bool r = wait_bar(bar, parity, abort_flag);
       return PAGED ? __all_sync(0xffffffffu, r) != 0 : r;
     };
     auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
@@ -1235,7 +1225,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     // Paged: after a wait that expired a warp only keeps its group's barriers, so that
     // none waits for another for ever.
     auto arrived = [&](uint64_t* bar, uint32_t parity) {
-      const bool r = wait_bar<PAGED>(bar, parity, abort_flag);
+      const bool r = wait_bar(bar, parity, abort_flag);
       return PAGED ? __all_sync(0xffffffffu, r) != 0 : r;
     };
     auto keep_vote = [&] { if (named_bar_or(bar2, 128, false)) named_bar_sync(bar1, 128); };

@@ -57,6 +57,8 @@ def definition(c):
         pos = torch.tensor([p for _, p in toks], device="cuda")
         keep = pos >= 0
         idx, pos = idx[keep], pos[keep]
+        if len(idx) == 0:
+            continue
         first, last = int(pos[0]), int(pos[-1])
         rows, lo, hi = [], [], []                              # a row is seen at positions lo .. hi - 1
         if c.W is not None:
