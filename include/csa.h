@@ -423,10 +423,13 @@ csa_status_t csa_grouped_out_proj(const void* o, const void* w_grp, const void* 
  * cudaMemcpy to the device: w_j = base^(-2j / rope_dim), stretched for contexts
  * `factor` (>= 1) times the trained one:
  *   original_len = 0: every frequency divided by factor (linear), mscale 1;
- *   original_len > 0: by parts (the published YaRN rule): with
+ *   original_len > 0: by parts (the rule of the YaRN paper): with
  *     turns = original_len * w_j / 2 pi and keep = (turns - beta_slow) /
  *     (beta_fast - beta_slow) limited to [0, 1],
  *     keep * w_j + (1 - keep) * w_j / factor; mscale = 0.1 ln(factor) + 1.
+ *     The ramp goes over the turns.  Models trained with a ramp over the pair's
+ *     index j between two correction dims need frequencies of their own: the other
+ *     calls take any.
  * inv_freq: rope_dim / 2 doubles.  No device call. */
 csa_status_t csa_rope_freqs(int rope_dim, double base, double factor, double original_len, double beta_fast,
                             double beta_slow, double* inv_freq, float* mscale);
@@ -463,7 +466,12 @@ csa_status_t csa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t q_hea
  *         [n_pages, page_size] = s (needs rope_dim 64): the row format of
  *         csa_compress_append.
  * A row without a page is not written and recorded as CSA_ERR_DEVICE.  A page
- * that is written belongs to one sequence. */
+ * that is written belongs to one sequence.
+ * Finished rows (the entries of csa_compress, normalised and turned already) go
+ * into entry pages with norm 0 and the entry's number as position: BF16 and F32
+ * without a rotation, E4M3 (whose rows need rope_dim 64) with frequencies of zero.
+ * csa_compress_append and csa_cache_append write dense caches, which are pages
+ * where cap is a multiple of the page size (see above). */
 csa_status_t csa_paged_append(const void* rows, csa_dtype_t in_dtype, int64_t row_stride, int64_t n_tok, int D,
                               const int32_t* cu_q, const int64_t* q_pos, int n_seq, const int32_t* block_table,
                               int max_pages, int page_size, int64_t n_pages, int norm, const float* gain, float eps,
@@ -493,9 +501,14 @@ csa_status_t csa_paged_append(const void* rows, csa_dtype_t in_dtype, int64_t ro
  * A visible row without a page is recorded as CSA_ERR_DEVICE, and the results of
  * the tokens that see it mean nothing; rows behind max_pages * page_size are not
  * visible.  A visible row with a NaN or an infinity puts NaN into the result.
- * workspace: csa_paged_attention_workspace(n_tok, n_seq, H, D) bytes (0 from
- * about 75 tokens or 385 sequences on), 16-byte aligned; calls sharing one must be ordered on
- * one stream, and a captured graph keeps its own. */
+ * workspace: csa_paged_attention_workspace(n_tok, n_seq, H, D) bytes (0 where rows
+ * are not split), 16-byte aligned; calls sharing one must be ordered on one stream,
+ * and a captured graph keeps its own.
+ * A token's rows are split over the SMs in batches of at most half as many tokens
+ * as SMs (74 of 148) and 384 sequences.  In larger ones a token, or the few
+ * tokens that share a pair of SMs, are the smallest piece of work: one long row set
+ * among short ones takes as long as one SM needs for it, and is better a call of
+ * its own. */
 size_t csa_paged_attention_workspace(int64_t n_tok, int n_seq, int H, int D);
 /* 1 if a call with these sizes works on pairs of SMs that share their rows, 0 if a
  * token at a time (max_pages 0: no such cache).  The two round differently, and the

@@ -528,7 +528,8 @@ def csa_rope_freqs(rope_dim, *, base=10000.0, factor=1.0, original_len=0, beta_f
                    device="cuda"):
     """Frequencies of the rotation, (inv_freq [rope_dim / 2] float64 on `device`,
     mscale): base^(-2j / rope_dim), stretched for a context `factor` times the
-    trained one: linearly (original_len 0), or by parts from the trained length."""
+    trained one: linearly (original_len 0), or by parts from the trained length,
+    with a ramp over the turns that a pair makes in it."""
     w = (ctypes.c_double * max(1, int(rope_dim) // 2))()
     ms = ctypes.c_float()
     _check(lib().csa_rope_freqs(int(rope_dim), base, factor, float(original_len), beta_fast, beta_slow,
@@ -645,7 +646,8 @@ def csa_paged_append(rows, cu_q, q_pos, block_table, pages, inv_freq, *, pages_r
     """Appends the raw rows [n_tok, D] of a ragged batch, normalised and rotated
     (inv_freq None: not rotated), to a paged cache: pages [n_pages, page_size, D]
     bfloat16 or float32, or uint8 e4m3 codes [n_pages, page_size, D - 64] with
-    pages_rope [.., 64] bfloat16 and pages_scale [n_pages, page_size] float32."""
+    pages_rope [.., 64] bfloat16 and pages_scale [n_pages, page_size] float32, which
+    need a rotation of 64 (frequencies of zero for rows that are turned already)."""
     what = "csa_paged_append"
     dev, n_seq = _batch(what, cu_q, q_pos, (rows, block_table, pages, inv_freq, pages_rope, pages_scale, gain))
     if rows.dim() != 2:
@@ -698,7 +700,9 @@ def csa_paged_attention(q, cu_q, q_pos, *, tok_pages=None, tok_table=None, W=128
     paged shared K = V rows: the complete entries (ratio m) of kv_pages (bfloat16
     [n_pages, page_size, D], or e4m3 with kv_rope and kv_scale) and the last W raw
     rows (0: all) of tok_pages, with the sink [H] in one softmax.  Either cache
-    may be absent.  The tokens' own raw rows are in their pages already."""
+    may be absent.  The tokens' own raw rows are in their pages already.  Rows are
+    split over the SMs in batches of at most half as many tokens as SMs: one token
+    with far more rows than the others of a larger batch is better a call of its own."""
     what = "csa_paged_attention"
     dev, n_seq = _batch(what, cu_q, q_pos, (q, tok_pages, tok_table, kv_pages, kv_rope, kv_scale, kv_table, sink, out,
                                             workspace))
@@ -866,7 +870,8 @@ def paged_layer_step(q, rows, cu_q, q_pos, inv_freq, tok_pages, tok_table, *, W=
     normalised and rotated, the raw rows [n_tok, D] appended to their token
     pages, the new tokens attend the window (W, 0: all raw rows) and, if
     kv_pages is given, the complete entries (a heavily compressed layer), and the
-    rotated part of the output is turned back (inv_rope)."""
+    rotated part of the output is turned back (inv_rope).  The entry pages are only
+    read: entries that this step completes are in them before (csa_paged_append)."""
     qn, _ = csa_qk_norm_rope(q, None, cu_q, q_pos, inv_freq, q_gain=q_gain, interleaved=interleaved, mscale=mscale,
                              eps=eps, out_dtype=torch.bfloat16, stream=stream)
     csa_paged_append(rows, cu_q, q_pos, tok_table, tok_pages, inv_freq, gain=gain, interleaved=interleaved,

@@ -57,9 +57,11 @@ def page_rows(store, table_row, lo, hi):
 
 def e4m3_page_rows(codes, rope, scale, table_row, lo, hi):
     """The rows as the attention reads them: codes * scale, and the RoPE part
-    divided by the scale, rounded to bf16 and multiplied by it again."""
+    divided by the scale, rounded to bf16 and multiplied by it again.  A scale
+    below 2^-100 (of a row that was zeroed and never written, say) counts as that."""
     c = e4m3_decode(page_rows(codes, table_row, lo, hi))
     s = page_rows(scale, table_row, lo, hi).astype(np.float32)[:, None]
+    s = np.where(np.abs(s) < 2.0 ** -100, np.float32(2.0 ** -100), s)
     r = page_rows(rope, table_row, lo, hi).astype(np.float32)
     turned = bf16_round(r * (np.float32(1) / s))
     return np.concatenate([c, turned], -1) * s.astype(np.float64)
