@@ -48,10 +48,11 @@
 // makes from the lengths on the device, and the ranges are merged; MMAs are issued
 // by whole warps with one elected lane; rows are prefetched into L2 ahead of the
 // ring.  16 sequences, 64 heads x 512, 9,700 to 28,900 raw rows each: 80 us, of
-// which the rows at the copy rate are 50 us, the plan, the first loads and the
-// merge about 20.  32 sequences over 820 to 7,900 e4m3 entries and a window of 128:
-// 66 us (rows 14 us): the conversion of a half chunk takes its loaders 4,000 cycles
-// of mostly latency, two groups of them in turn.
+// which the rows at the copy rate are 50 us, the plan, the first loads, the last
+// epilogue and the merge about 25.  32 sequences over 820 to 7,900 e4m3 entries and a
+// window of 128: 66 us (rows 14 us): a slot holds K and V of a half chunk, so its
+// loaders convert the next one only after S, softmax and PV of this one; with two
+// slots, each with loaders of its own, some 4,000 cycles a half chunk and SM.
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -82,8 +83,8 @@ constexpr int kThreads = 352;      // 11 warps: 4 softmax + epilogue, 4 loaders,
 // Paged calls have 4 more warps (11 - 14).  E4M3: a second group of loaders; the
 // groups take alternate half chunks, so one group's loads are in flight while the
 // other converts.  BF16: a second group for the softmax and the output, with
-// columns (heads) 32 .. 63 (3,500 tokens of 64 heads, window 128: 156 us against
-// 180 with one).
+// columns (heads) 32 .. 63 (3,500 tokens of 64 heads, window 128: 161 us against
+// 183 with one).
 template <bool PAGED>
 constexpr int attn_threads() { return PAGED ? kThreads + 128 : kThreads; }
 constexpr int kNQ = 64;            // query rows (heads) per tile = MMA N

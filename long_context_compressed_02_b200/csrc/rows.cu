@@ -155,10 +155,13 @@ __device__ __forceinline__ int find_seq(const int32_t* cu_q, int n_seq, int64_t 
 // UPL: units per lane; K: row groups (32 / lpr rows) in flight per warp.
 // Two groups and 24 warps an SM (80 registers) were the best of the measured
 // splits: 4,850 tokens of 64 + 1 rows of 512 bf16 take 122 us (5.4 TB/s, 0.82 of
-// the copy rate) against 168 us with 32 warps (64 registers, spills) and 162 us
-// with four groups and 16 warps; 11,700 tokens of 64 rows of 128, turned whole,
-// 76 us (5.35 TB/s).  The issue slots, not DRAM, were full before the float32
-// pairs (mul2, fma2) and the shared look-ups: 390 instructions a row, 142 us.
+// the copy rate; the bf16 instances spill up to 9 registers) against 168 us with 32
+// warps (64 registers, more spills) and 162 us with four groups and 16 warps;
+// 11,700 tokens of 64 rows of 128, turned whole, 76 us (5.35 TB/s).  The issue
+// slots, not DRAM, were full before the float32 pairs (mul2, fma2) and the shared
+// look-ups: 390 instructions a row, 142 us.  Appended prompt rows share no look-up:
+// 26,900 of 512 take 18 us into bf16 pages (12 us without the rotation) and 21 us into
+// e4m3 pages, with 59 and 64 % of the issue slots taken while they run.
 template <typename Tin, typename Tout, int UPL, int K, int DEST>
 __global__ void __launch_bounds__(32 * kMaxWarps, UPL == 4 ? 1 : sizeof(Tin) * UPL > 2 ? 2 : 3)
 rows_kernel(const __grid_constant__ RowsParams p) {
