@@ -1532,6 +1532,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
     }
   }
   __syncwarp();                 // reconverge role warps before the CTA barrier
+  drain_after_abort(abort_flag);
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {

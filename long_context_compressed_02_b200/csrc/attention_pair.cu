@@ -822,11 +822,7 @@ pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ PairMa
     __syncwarp();
   }
   __syncwarp();
-  if (*abort_flag) {                                         // copies in flight land before shared memory goes
-    const uint64_t t0 = global_ns();
-    while (global_ns() - t0 < 1000000ull) {}
-  }
-  __syncwarp();
+  drain_after_abort(abort_flag);
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                            // neither CTA leaves while the other may reach it

@@ -696,6 +696,7 @@ indexer_scores_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
     }
   }
   __syncwarp();                 // reconverge role warps before the CTA barrier
+  drain_after_abort(abort_flag);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -192,6 +192,7 @@ proj_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
     }
   }
   __syncwarp();
+  drain_after_abort(abort_flag);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

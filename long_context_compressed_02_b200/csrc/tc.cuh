@@ -80,6 +80,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   return false;
 }
 
+// At the end of a kernel, before its shared memory and TMEM go: if one of the CTA's
+// waits expired, whatever copies and products it has in flight get 1 ms to land.
+__device__ __forceinline__ void drain_after_abort(volatile int* abort_flag) {
+  if (*abort_flag) {
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 1000000ull) {}
+  }
+  __syncwarp();
+}
+
 // ---------------------------------------------------------------- dependent launch
 // Wait until the previous kernel on the stream has completed and its writes
 // are visible (a no-op for a kernel launched without the dependent attribute).
