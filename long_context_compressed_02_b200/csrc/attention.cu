@@ -595,7 +595,7 @@ attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtens
   // Warps from 11 on, where there are any, load or share the softmax.  The loaders are
   // "all others" for dense calls too: with 4 .. 7 alone the compiler lays the roles
   // out so that the gathered decode attention (16 tokens, 512 entries and a window of
-  // 128) takes 38 us, 32 so.
+  // 128) takes 36 us, 32 so.
   if ((warp >= 4 && warp < 8) || (!kTwo && warp >= 11)) {
     // ============================ loaders
     const int grp = warp >= 11 ? 1 : 0;
